@@ -1,11 +1,14 @@
 """Python binding of the sm_100a dynamic-convolution C ABI (``include/dynconv.h``,
-``include/dynconv_backward.h``, ``include/dynconv_cells.h``).
+``include/dynconv_backward.h``, ``include/dynconv_cells.h``,
+``include/dynconv_train.h``).
 
 Argument marshalling only: every function forwards to the symbol of the same
 name in ``libdynconv.so``; all arithmetic runs in the library's CUDA kernels.
-Tensors may be passed as torch CUDA tensors (their data pointers are taken) or
-as raw integer device addresses. There is no CPU fallback: if the library is
-missing or no sm_100 device is present, the calls raise.
+``train_tensor`` also checks the torch tensors it is given, since a list keeps
+their addresses and element counts. Tensors may be passed as torch CUDA tensors
+(their data pointers are taken) or as raw integer device addresses. There is no
+CPU fallback: if the library is missing or no sm_100 device is present, the
+calls raise.
 """
 from __future__ import annotations
 
@@ -36,12 +39,34 @@ SYMBOLS = ("dynconv_route", "dynconv_forward", "dynconv_forward_noalloc",
            "dynconv_route_backward", "dynconv_backward_data",
            # include/dynconv_cells.h
            "dynconv_route_cells", "dynconv_cells_workspace_size", "dynconv_forward_cells")
+# include/dynconv_train.h
+TRAIN_SYMBOLS = ("dynconv_balance_workspace_size", "dynconv_balance_forward",
+                 "dynconv_balance_backward", "dynconv_grad_norm_workspace_size",
+                 "dynconv_grad_norm", "dynconv_adamw")
 
 
 class dynconv_desc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in
                 ("B", "C_in", "H", "W", "C_out", "KH", "KW", "stride", "pad", "groups", "n",
                  "dtype", "variant")]
+
+
+class dynconv_balance_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("rows", "groups", "n", "top_k", "mode")] + \
+        [("row_stride", ctypes.c_longlong)]
+
+
+class dynconv_train_tensor(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in
+                ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+        [("numel", ctypes.c_longlong)] + \
+        [(f, ctypes.c_int) for f in ("dtype", "grad_dtype", "state_bits")] + \
+        [(f, ctypes.c_float) for f in ("lr_scale", "weight_decay")]
+
+
+class dynconv_adamw_hyper(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps")] + \
+        [("step", ctypes.c_longlong), ("seed", ctypes.c_uint)]
 
 
 class DynconvError(RuntimeError):
@@ -110,6 +135,23 @@ def load():
         lib.dynconv_cells_workspace_size.restype = ctypes.c_size_t
         lib.dynconv_forward_cells.argtypes = [D, ctypes.c_int, P, P, P, P, P, P, ctypes.c_size_t, P]
         lib.dynconv_forward_cells.restype = ctypes.c_int
+        BD, TT = ctypes.POINTER(dynconv_balance_desc), ctypes.POINTER(dynconv_train_tensor)
+        lib.dynconv_balance_workspace_size.argtypes = [BD]
+        lib.dynconv_balance_workspace_size.restype = ctypes.c_size_t
+        lib.dynconv_balance_forward.argtypes = [BD, P, P, ctypes.c_float, P, P, P, P, P,
+                                                ctypes.c_size_t, P]
+        lib.dynconv_balance_forward.restype = ctypes.c_int
+        lib.dynconv_balance_backward.argtypes = [BD, P, P, ctypes.c_float, P, P, P, P,
+                                                 ctypes.c_longlong, ctypes.c_int, P]
+        lib.dynconv_balance_backward.restype = ctypes.c_int
+        lib.dynconv_grad_norm_workspace_size.argtypes = [ctypes.c_int]
+        lib.dynconv_grad_norm_workspace_size.restype = ctypes.c_size_t
+        lib.dynconv_grad_norm.argtypes = [TT, ctypes.c_int, ctypes.c_double, P, P, P,
+                                          ctypes.c_size_t, P]
+        lib.dynconv_grad_norm.restype = ctypes.c_int
+        lib.dynconv_adamw.argtypes = [TT, ctypes.c_int, ctypes.POINTER(dynconv_adamw_hyper), P, P,
+                                      P, P]
+        lib.dynconv_adamw.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -289,3 +331,117 @@ def dynconv_forward_cells(desc, cells, x, warehouse, alpha, bias, y, workspace, 
     return load().dynconv_forward_cells(ctypes.byref(desc), int(cells), _ptr(x), _ptr(warehouse),
                                         _ptr(alpha), _ptr(bias), _ptr(y), _ptr(workspace),
                                         int(workspace_bytes), _stream(stream))
+
+
+# ------------------------------------------------------------------ training
+
+
+def make_balance_desc(rows, n, groups=1, top_k=1, mode=SOFTMAX,
+                      row_stride=None) -> dynconv_balance_desc:
+    return dynconv_balance_desc(int(rows), int(groups), int(n), int(top_k), int(mode),
+                                int(groups) * int(n) if row_stride is None else int(row_stride))
+
+
+def dynconv_balance_workspace_size(desc) -> int:
+    return load().dynconv_balance_workspace_size(ctypes.byref(desc))
+
+
+def dynconv_balance_forward(desc, alpha, row_mask, coef, counts, mean, rows_kept, loss, workspace,
+                            workspace_bytes, stream=None) -> int:
+    """counts int32 [groups][n], mean fp32 [groups][n], rows_kept int32 [1] and
+    loss fp32 [1] of the attentions alpha [rows][groups][n]; row_mask: one byte
+    (or bool) per row, nonzero = kept, or None."""
+    return load().dynconv_balance_forward(ctypes.byref(desc), _ptr(alpha), _ptr(row_mask),
+                                          float(coef), _ptr(counts), _ptr(mean), _ptr(rows_kept),
+                                          _ptr(loss), _ptr(workspace), int(workspace_bytes),
+                                          _stream(stream))
+
+
+def dynconv_balance_backward(desc, alpha, row_mask, coef, counts, rows_kept, dloss, dalpha,
+                             dalpha_stride, accumulate, stream=None) -> int:
+    """dalpha [rows][groups][n], rows dalpha_stride floats apart: added to
+    (accumulate) or overwritten. dloss fp32 [1] on the device, or None for 1."""
+    return load().dynconv_balance_backward(ctypes.byref(desc), _ptr(alpha), _ptr(row_mask),
+                                           float(coef), _ptr(counts), _ptr(rows_kept),
+                                           _ptr(dloss), _ptr(dalpha), int(dalpha_stride),
+                                           int(accumulate), _stream(stream))
+
+
+def train_tensor(grad, param=None, m=None, v=None, master=None, m_scale=None, v_scale=None,
+                 lr_scale=1.0, weight_decay=0.0) -> dynconv_train_tensor:
+    """One entry of a list for dynconv_grad_norm (grad alone is enough) and
+    dynconv_adamw, from contiguous torch CUDA tensors of one device: types and
+    sizes are read from them (8-bit states where m is a one-byte type), and a
+    tensor that does not fit raises ValueError."""
+    import torch
+    types = {torch.float32: F32, torch.bfloat16: BF16}
+    numel = grad.numel()
+
+    def check(name, t, dtypes, count=numel):
+        if t is None:
+            return
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: {t.dtype} is not one of {tuple(dtypes)}")
+        if t.numel() != count:
+            raise ValueError(f"{name}: {t.numel()} elements, {count} expected")
+        if not t.is_contiguous() or t.device != grad.device:
+            raise ValueError(f"{name}: must be contiguous and on {grad.device}")
+
+    check("grad", grad, types)
+    check("param", param, types)
+    check("master", master, (torch.float32,))
+    if (param is None) != (m is None) or (param is None) != (v is None):
+        raise ValueError("param, m and v are given together")
+    bits = 32
+    if m is not None:
+        bits = 8 * m.element_size()
+        states = ((torch.float32,) if bits == 32
+                  else (torch.float8_e4m3fn, torch.uint8))
+        check("m", m, states)
+        check("v", v, states)
+        if bits == 8 and (m_scale is None or v_scale is None):
+            raise ValueError("8-bit states need m_scale and v_scale")
+        if bits == 32 and (m_scale is not None or v_scale is not None):
+            raise ValueError("32-bit states take no scales")
+        check("m_scale", m_scale, (torch.float32,), -(-numel // 256))
+        check("v_scale", v_scale, (torch.float32,), -(-numel // 256))
+        if master is not None and param.dtype != torch.bfloat16:
+            raise ValueError("a master copy goes with a bf16 param")
+    return dynconv_train_tensor(
+        _ptr(param), _ptr(master), _ptr(grad), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale),
+        numel, F32 if param is None else types[param.dtype], types[grad.dtype], bits,
+        float(lr_scale), float(weight_decay))
+
+
+def train_tensors(entries):
+    """The list that dynconv_grad_norm and dynconv_adamw take. It holds addresses:
+    the tensors must stay where they are while it is used."""
+    entries = list(entries)
+    return (dynconv_train_tensor * len(entries))(*entries)
+
+
+def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0) -> dynconv_adamw_hyper:
+    return dynconv_adamw_hyper(float(lr), float(beta1), float(beta2), float(eps), int(step),
+                               int(seed) & 0xFFFFFFFF)
+
+
+def dynconv_grad_norm_workspace_size(tensors) -> int:
+    """Workspace bytes for a list from train_tensors, or for a number of tensors."""
+    count = tensors if isinstance(tensors, int) else len(tensors)
+    return load().dynconv_grad_norm_workspace_size(count)
+
+
+def dynconv_grad_norm(tensors, max_norm, stats, step, workspace, workspace_bytes,
+                      stream=None) -> int:
+    """stats fp32 [2] = {norm of all gradients, factor that clips it to max_norm};
+    step int64 [1] (or None) is increased by one unless the norm is not finite."""
+    return load().dynconv_grad_norm(tensors, len(tensors), float(max_norm), _ptr(stats),
+                                    _ptr(step), _ptr(workspace), int(workspace_bytes),
+                                    _stream(stream))
+
+
+def dynconv_adamw(tensors, hyper, grad_scale=None, lr=None, step=None, stream=None) -> int:
+    """One AdamW step over the list, in place; grad_scale, lr (fp32 [1]) and step
+    (int64 [1]) on the device replace 1 and the values in hyper."""
+    return load().dynconv_adamw(tensors, len(tensors), ctypes.byref(hyper), _ptr(grad_scale),
+                                _ptr(lr), _ptr(step), _stream(stream))

@@ -1,10 +1,10 @@
 """Build the sm_100a C-ABI library ``libdynconv.so`` in-tree with nvcc.
 
 Usage: ``python -m dynamic_convolution_b200.build`` (or ``build()`` from Python).
-The library has three translation units: ``csrc/dynconv.cu`` (the forward
+The library has four translation units: ``csrc/dynconv.cu`` (the forward
 entry points; it includes the forward kernel headers), ``csrc/backward.cu``
-(the backward entry points and kernels) and ``csrc/cells.cu`` (warehouse
-cells); it links the CUDA runtime statically and reaches the driver's
+(the backward entry points and kernels), ``csrc/cells.cu`` (warehouse cells)
+and ``csrc/train.cu`` (balance loss, gradient norm, AdamW); it links the CUDA runtime statically and reaches the driver's
 tensor-map encoder through the runtime's entry-point query, so it loads on a
 machine without a GPU driver (the calls then fail with DYNCONV_ERR_CUDA).
 """
@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdynconv.so")
 UNITS = [os.path.join(CSRC, "dynconv.cu"), os.path.join(CSRC, "backward.cu"),
-         os.path.join(CSRC, "cells.cu")]
+         os.path.join(CSRC, "cells.cu"), os.path.join(CSRC, "train.cu")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
