@@ -25,25 +25,34 @@ size_t align16(size_t v) { return (v + 15) & ~size_t(15); }
 
 // Launch with a programmatic edge: the kernel may be scheduled while the
 // previous one on the stream finishes, and waits for it (griddepcontrol.wait)
-// before it touches global memory.
+// before it touches global memory. cluster > 1: that many CTAs to a cluster.
 template <typename Kern, typename... Args>
-int launch(const char* what, Kern kern, dim3 grid, int threads, cudaStream_t stream,
-           const Args&... args) {
+int launch_cluster(const char* what, Kern kern, dim3 grid, int cluster, int threads, size_t smem,
+                   cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return dc_lib::cuda_error(e, what);
   }
   return dc_lib::launched(what);
+}
+template <typename Kern, typename... Args>
+int launch(const char* what, Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+           const Args&... args) {
+  return launch_cluster(what, kern, grid, 1, threads, smem, stream, args...);
 }
 
 // ------------------------------------------------------------------- balance
@@ -67,11 +76,20 @@ int row_lanes(int n) {
   return lanes;
 }
 
-// Parts of the forward's sums: CTAs per group, about two per SM of 148 in all.
+// The whole forward in one launch of one cluster of up to eight CTAs, each taking
+// every eighth group: while the busiest of them has at most 32 K attentions.
+bool balance_small(const dynconv_balance_desc* d) {
+  const long long turns = (d->groups + dct::kBalCluster - 1) / dct::kBalCluster;
+  return turns * d->rows * d->n <= 32768;
+}
+
+// Parts of the forward's sums: CTAs per group, as many in all as run at a time
+// on 148 SMs.
 int balance_parts(const dynconv_balance_desc* d) {
   const long long per = dct::kBalWarps * (32 / row_lanes(d->n));
   const long long want = (d->rows + per - 1) / per;
-  return static_cast<int>(std::max(1LL, std::min<long long>(want, 296 / d->groups)));
+  const long long most = (d->n <= 256 ? 592 : 296) / d->groups;
+  return static_cast<int>(std::max(1LL, std::min(want, most)));
 }
 
 size_t balance_bytes(const dynconv_balance_desc* d) {
@@ -100,7 +118,17 @@ struct LaunchForward {
   template <int L, int V>
   int operator()() const {
     return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V>, grid,
-                  dct::kBalThreads, s, p);
+                  dct::kBalThreads, 0, s, p);
+  }
+};
+struct LaunchSmall {
+  int ctas;
+  cudaStream_t s;
+  const dct::BalParams& p;
+  template <int L, int V>
+  int operator()() const {
+    return launch_cluster("balance_small_kernel", dct::balance_small_kernel<L, V>, dim3(ctas), ctas,
+                          dct::kBalThreads, 0, s, p);
   }
 };
 struct LaunchSigmoid {
@@ -110,7 +138,7 @@ struct LaunchSigmoid {
   template <int L, int V>
   int operator()() const {
     return launch("balance_backward_sigmoid_kernel", dct::balance_backward_sigmoid_kernel<L, V>,
-                  grid, dct::kBalThreads, s, p);
+                  grid, dct::kBalThreads, 0, s, p);
   }
 };
 
@@ -121,6 +149,7 @@ constexpr int kAdamCap = 360;   // in the long one (32764 bytes of kernel parame
 static_assert(sizeof(dct::AdamTable<kAdamCap>) <= 32764, "kernel parameters");
 
 constexpr long long kMaxNumel = 1LL << 40;
+constexpr double kMinEps = 1.1754943508222875e-38;  // 2^-126
 
 bool valid_dtype(int t) { return t == DYNCONV_F32 || t == DYNCONV_BF16; }
 size_t size_of(int dtype) { return dtype == DYNCONV_F32 ? 4 : 2; }
@@ -177,18 +206,24 @@ int check_state(const dynconv_train_tensor& t) {
   return DYNCONV_OK;
 }
 
-long long chunks_of(long long numel) { return (numel + dct::kChunk - 1) / dct::kChunk; }
+long long units_of(long long numel, long long unit) { return (numel + unit - 1) / unit; }
 
 // Four elements of the type are one load of 4 * size bytes.
 bool vec_ok(const void* p, size_t elem) { return aligned(p, 4 * elem); }
 
-template <int CAP>
+template <int CAP, bool HAS8>
 int launch_adam(const dct::AdamShared& h, const dct::AdamEntry* e, int sms, cudaStream_t s) {
+  using Shape = dct::AdamShape<HAS8>;
+  const auto kern = dct::adamw_kernel<CAP, HAS8>;
+  if (Shape::smem > 0) {
+    const cudaError_t err = dc_lib::set_smem(reinterpret_cast<const void*>(kern), Shape::smem);
+    if (err != cudaSuccess) return dc_lib::cuda_error(err, "cudaFuncSetAttribute(adamw)");
+  }
   dct::AdamTable<CAP> t;
   t.h = h;
   std::copy(e, e + h.count, t.e);
-  const int grid = static_cast<int>(std::min<long long>(h.chunks, 1LL * sms * 4));
-  return launch("adamw_kernel", dct::adamw_kernel<CAP>, dim3(grid), dct::kOptThreads, s, t);
+  const int grid = static_cast<int>(std::min<long long>(h.chunks, 1LL * sms * Shape::ctas));
+  return launch("adamw_kernel", kern, dim3(grid), dct::kOptThreads, Shape::smem, s, t);
 }
 
 }  // namespace
@@ -231,7 +266,14 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   p.part_sum = reinterpret_cast<double*>(ws);
   p.part_count = reinterpret_cast<int*>(ws + align16(parts * width * 8));
   p.part_kept = reinterpret_cast<int*>(ws + align16(parts * width * 8) + align16(parts * width * 4));
+  p.coef = coef;
+  p.counts = counts;
+  p.mean = mean;
+  p.rows_kept = rows_kept;
+  p.loss = loss;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (balance_small(desc))
+    return with_layout(desc->n, LaunchSmall{std::min(desc->groups, dct::kBalCluster), s, p});
   rc = with_layout(desc->n, LaunchForward{dim3(parts, desc->groups), s, p});
   if (rc) return rc;
   dct::BalFinish f{};
@@ -248,8 +290,14 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   f.mean = mean;
   f.rows_kept = rows_kept;
   f.loss = loss;
-  return launch("balance_finish_kernel", dct::balance_finish_kernel, dim3(1),
-                dct::kBalFinishThreads, s, f);
+  // columns side by side: enough for 32-byte rows of parts, few enough that the
+  // parts are split over many threads
+  f.tile = 16;
+  while (f.tile < 64 && f.tile < static_cast<int>(width)) f.tile *= 2;
+  const int tiles = (static_cast<int>(width) + f.tile - 1) / f.tile;
+  const int ctas = std::min(tiles, dct::kBalCluster);
+  return launch_cluster("balance_finish_kernel", dct::balance_finish_kernel, dim3(ctas), ctas,
+                        dct::kBalFinishThreads, 0, s, f);
 }
 
 int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alpha,
@@ -306,7 +354,7 @@ int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alph
   const long long want = (desc->rows + ty - 1) / ty;
   const int gx = static_cast<int>(std::min<long long>(want, std::max(1LL, 8LL * di.sms / gy)));
   return launch("balance_backward_softmax_kernel", dct::balance_backward_softmax_kernel,
-                dim3(gx, gy), dct::kBalThreads, s, p, tx);
+                dim3(gx, gy), dct::kBalThreads, 0, s, p, tx);
 }
 
 size_t dynconv_grad_norm_workspace_size(int count) {
@@ -333,9 +381,9 @@ int dynconv_grad_norm(const dynconv_train_tensor* tensors, int count, double max
   double* part = static_cast<double*>(workspace);
   int parts = 0;
   for (int i = 0; i < count;) {
-    dct::NormTable t;
+    dct::NormTable<dct::kNormCap> t;
     t.count = 0;
-    t.chunks = 0;
+    t.units = 0;
     t.part = part + parts;
     for (; i < count && t.count < dct::kNormCap; ++i) {
       const dynconv_train_tensor& a = tensors[i];
@@ -343,19 +391,30 @@ int dynconv_grad_norm(const dynconv_train_tensor* tensors, int count, double max
       dct::NormEntry& e = t.e[t.count++];
       e.grad = a.grad;
       e.numel = a.numel;
-      e.first_chunk = t.chunks;
+      e.first = t.units;
       e.bf16 = a.grad_dtype == DYNCONV_BF16;
-      e.vec = vec_ok(a.grad, size_of(a.grad_dtype));
-      t.chunks += chunks_of(a.numel);
+      e.vec = aligned(a.grad, 16);
+      t.units += units_of(a.numel, dct::kNormUnit);
     }
     if (t.count == 0) break;
-    const int grid = static_cast<int>(std::min<long long>(t.chunks, dct::kNormParts));
-    rc = launch("grad_norm_kernel", dct::grad_norm_kernel, dim3(grid), dct::kOptThreads, s, t);
+    const int grid = static_cast<int>(std::min<long long>(t.units, dct::kNormParts));
+    if (t.count <= kSmallCap) {
+      dct::NormTable<kSmallCap> few;
+      std::copy(t.e, t.e + t.count, few.e);
+      few.units = t.units;
+      few.count = t.count;
+      few.part = t.part;
+      rc = launch("grad_norm_kernel", dct::grad_norm_kernel<kSmallCap>, dim3(grid),
+                  dct::kOptThreads, 0, s, few);
+    } else {
+      rc = launch("grad_norm_kernel", dct::grad_norm_kernel<dct::kNormCap>, dim3(grid),
+                  dct::kOptThreads, 0, s, t);
+    }
     if (rc) return rc;
     parts += grid;
   }
   return launch("grad_norm_finish_kernel", dct::grad_norm_finish_kernel, dim3(1),
-                dct::kOptThreads, s, static_cast<const double*>(part), parts, max_norm, stats,
+                dct::kOptThreads, 0, s, static_cast<const double*>(part), parts, max_norm, stats,
                 step);
 }
 
@@ -365,7 +424,7 @@ int dynconv_adamw(const dynconv_train_tensor* tensors, int count,
   if (count < 0 || (count > 0 && !tensors) || !hyper) return DYNCONV_ERR_INVALID_ARG;
   const auto beta_ok = [](double b) { return b >= 0 && b < 1; };
   if (!(hyper->lr >= 0) || !std::isfinite(hyper->lr) || !beta_ok(hyper->beta1) ||
-      !beta_ok(hyper->beta2) || !(hyper->eps > 0) || !std::isfinite(hyper->eps) ||
+      !beta_ok(hyper->beta2) || !(hyper->eps >= kMinEps) || !(hyper->eps <= 1e30) ||
       (!step && hyper->step < 1))
     return DYNCONV_ERR_INVALID_ARG;
   for (int i = 0; i < count; ++i) {
@@ -392,16 +451,20 @@ int dynconv_adamw(const dynconv_train_tensor* tensors, int count,
   h.grad_scale = grad_scale;
   h.lr_dev = lr;
   h.step_dev = step;
-  if (!step) {
-    h.step = hyper->step;
-    h.inv_bc1 = 1.0 / (1.0 - std::pow(hyper->beta1, static_cast<double>(hyper->step)));
-    h.root2 = 1.0 / std::sqrt(1.0 - std::pow(hyper->beta2, static_cast<double>(hyper->step)));
+  h.step = hyper->step;
+  h.dynamic = lr || step;
+  double inv_bc1 = 0.0;
+  if (!h.dynamic) {
+    const double t = static_cast<double>(hyper->step);
+    inv_bc1 = 1.0 / (1.0 - std::pow(hyper->beta1, t));
+    h.root2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(hyper->beta2, t)));
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   dct::AdamEntry entries[kAdamCap];
   for (int i = 0; i < count;) {
     h.count = 0;
     h.chunks = 0;
+    bool has8 = false;
     for (; i < count && h.count < kAdamCap; ++i) {
       const dynconv_train_tensor& a = tensors[i];
       if (a.numel == 0) continue;
@@ -414,10 +477,16 @@ int dynconv_adamw(const dynconv_train_tensor* tensors, int count,
       e.m_scale = a.m_scale;
       e.v_scale = a.v_scale;
       e.numel = a.numel;
-      e.first_chunk = h.chunks;
-      e.lr_scale = a.lr_scale;
-      e.decay = a.weight_decay;
+      e.first = h.chunks;
+      e.size = a.lr_scale;
+      e.keep = a.weight_decay;
+      if (!h.dynamic) {
+        const double rate = hyper->lr * a.lr_scale;
+        e.size = static_cast<float>(rate * inv_bc1);
+        e.keep = static_cast<float>(1.0 - rate * a.weight_decay);
+      }
       e.place = i;
+      has8 = has8 || a.state_bits == 8;
       const int param = a.dtype == DYNCONV_F32 ? dct::kParamF32
                                                : a.master ? dct::kParamMaster : dct::kParamBf16;
       const size_t st = a.state_bits == 8 ? 1 : 4;
@@ -425,11 +494,15 @@ int dynconv_adamw(const dynconv_train_tensor* tensors, int count,
                        vec_ok(a.grad, size_of(a.grad_dtype)) && vec_ok(a.m, st) && vec_ok(a.v, st);
       e.kind = param | (a.grad_dtype == DYNCONV_BF16 ? 4 : 0) | (a.state_bits == 8 ? 8 : 0) |
                (vec ? 16 : 0);
-      h.chunks += chunks_of(a.numel);
+      h.chunks += units_of(a.numel, dct::kChunk);
     }
     if (h.count == 0) break;
-    rc = h.count <= kSmallCap ? launch_adam<kSmallCap>(h, entries, di.sms, s)
-                              : launch_adam<kAdamCap>(h, entries, di.sms, s);
+    if (h.count <= kSmallCap)
+      rc = has8 ? launch_adam<kSmallCap, true>(h, entries, di.sms, s)
+                : launch_adam<kSmallCap, false>(h, entries, di.sms, s);
+    else
+      rc = has8 ? launch_adam<kAdamCap, true>(h, entries, di.sms, s)
+                : launch_adam<kAdamCap, false>(h, entries, di.sms, s);
     if (rc) return rc;
   }
   return DYNCONV_OK;

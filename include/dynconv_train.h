@@ -173,7 +173,7 @@ int dynconv_grad_norm(const dynconv_train_tensor* tensors, int count, double max
  * its bits to an even element and the high half to an odd one (from element 2^33
  * on, K ^= F(element >> 33) first). The same inputs give the same bits.
  *
- * lr >= 0, 0 <= beta < 1, eps > 0, step >= 1. */
+ * lr >= 0, 0 <= beta < 1, 2^-126 <= eps <= 1e30, step >= 1. */
 typedef struct {
   double lr, beta1, beta2, eps;
   long long step;
