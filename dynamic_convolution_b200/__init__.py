@@ -374,42 +374,44 @@ def train_tensor(grad, param=None, m=None, v=None, master=None, m_scale=None, v_
     sizes are read from them (8-bit states where m is a one-byte type), and a
     tensor that does not fit raises ValueError."""
     import torch
-    types = {torch.float32: F32, torch.bfloat16: BF16}
-    numel = grad.numel()
+    f32, bf16, numel, device = torch.float32, torch.bfloat16, grad.numel(), grad.device
 
-    def check(name, t, dtypes, count=numel):
-        if t is None:
-            return
+    def check(name, t, dtypes, count):
         if t.dtype not in dtypes:
-            raise ValueError(f"{name}: {t.dtype} is not one of {tuple(dtypes)}")
+            raise ValueError(f"{name}: {t.dtype} is not one of {dtypes}")
         if t.numel() != count:
             raise ValueError(f"{name}: {t.numel()} elements, {count} expected")
-        if not t.is_contiguous() or t.device != grad.device:
-            raise ValueError(f"{name}: must be contiguous and on {grad.device}")
+        if not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name}: must be contiguous and on {device}")
 
-    check("grad", grad, types)
-    check("param", param, types)
-    check("master", master, (torch.float32,))
-    if (param is None) != (m is None) or (param is None) != (v is None):
-        raise ValueError("param, m and v are given together")
-    bits = 32
-    if m is not None:
+    check("grad", grad, (f32, bf16), numel)
+    bits, dtype = 32, F32
+    if param is None:
+        if not (m is v is master is m_scale is v_scale is None):
+            raise ValueError("param, m and v are given together")
+    else:
+        if m is None or v is None:
+            raise ValueError("param, m and v are given together")
+        check("param", param, (f32, bf16), numel)
+        dtype = F32 if param.dtype is f32 else BF16
         bits = 8 * m.element_size()
-        states = ((torch.float32,) if bits == 32
-                  else (torch.float8_e4m3fn, torch.uint8))
-        check("m", m, states)
-        check("v", v, states)
-        if bits == 8 and (m_scale is None or v_scale is None):
-            raise ValueError("8-bit states need m_scale and v_scale")
-        if bits == 32 and (m_scale is not None or v_scale is not None):
+        states = (f32,) if bits == 32 else (torch.float8_e4m3fn, torch.uint8)
+        check("m", m, states, numel)
+        check("v", v, states, numel)
+        if bits == 8:
+            if m_scale is None or v_scale is None:
+                raise ValueError("8-bit states need m_scale and v_scale")
+            check("m_scale", m_scale, (f32,), -(-numel // 256))
+            check("v_scale", v_scale, (f32,), -(-numel // 256))
+        elif m_scale is not None or v_scale is not None:
             raise ValueError("32-bit states take no scales")
-        check("m_scale", m_scale, (torch.float32,), -(-numel // 256))
-        check("v_scale", v_scale, (torch.float32,), -(-numel // 256))
-        if master is not None and param.dtype != torch.bfloat16:
-            raise ValueError("a master copy goes with a bf16 param")
+        if master is not None:
+            if dtype != BF16:
+                raise ValueError("a master copy goes with a bf16 param")
+            check("master", master, (f32,), numel)
     return dynconv_train_tensor(
         _ptr(param), _ptr(master), _ptr(grad), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale),
-        numel, F32 if param is None else types[param.dtype], types[grad.dtype], bits,
+        numel, dtype, F32 if grad.dtype is f32 else BF16, bits,
         float(lr_scale), float(weight_decay))
 
 

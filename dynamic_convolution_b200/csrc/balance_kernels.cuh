@@ -1,10 +1,12 @@
 // Kernels of the router's load-balance loss (include/dynconv_train.h).
 //
 // A row of n attentions is held by L neighbouring lanes of a warp, V values in
-// each lane's registers (n <= L * V), so a warp holds 32 / L rows: lane l of a
-// row owns the elements (c * L + l) * 4 + q, c = 0.., q = 0..3 (four to a chunk c),
-// which 16-byte loads fetch contiguously. More values per lane mean fewer steps
-// across lanes, which the top k need in every round.
+// each lane's registers (n <= L * V), so a warp holds 32 / L rows. More values per
+// lane mean fewer steps across lanes, which the top k need in every round. Up to
+// V = 8 lane l of a row owns the elements l V .. l V + V - 1, so that the lowest
+// index among equals is the lowest lane's; above, 16-byte loads at that distance
+// would waste the L1, and it owns (c * L + l) * 4 + q, c = 0.., q = 0..3 (chunks c
+// of four).
 #pragma once
 
 #include <climits>
@@ -15,7 +17,9 @@
 namespace dct {
 
 constexpr int kBalThreads = 256;
-constexpr int kBalWarps = kBalThreads / 32;
+// Threads of a forward CTA that has an SM to itself, so that few parts are left to
+// be added; where those do not fill the GPU the CTAs have kBalThreads.
+constexpr int forward_threads(int values) { return values <= 8 ? 1024 : 512; }
 constexpr int kBalMaxN = 1024;
 constexpr int kBalMaxTopK = 32;
 constexpr int kBalCluster = 8;          // CTAs of a cluster at most
@@ -51,13 +55,18 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+template <int L, int V>
+__device__ __forceinline__ int element_of(int slot, int lane) {
+  return V <= 8 ? lane * V + slot : ((slot >> 2) * L + lane) * 4 + (slot & 3);
+}
+
 // The lane's V elements of a row (0 where the row ends or `live` is false).
 template <int L, int V>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int n, int lane, bool vec,
                                          bool live, float (&a)[V]) {
 #pragma unroll
   for (int c = 0; c < V / 4; ++c) {
-    const int e = (c * L + lane) * 4;
+    const int e = element_of<L, V>(4 * c, lane);
     if (vec) {  // n is a multiple of 4 here
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (live && e < n) f = *reinterpret_cast<const float4*>(row + e);
@@ -67,11 +76,6 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int n, i
       for (int q = 0; q < 4; ++q) a[4 * c + q] = live && e + q < n ? row[e + q] : 0.f;
     }
   }
-}
-
-template <int L, int V>
-__device__ __forceinline__ int element_of(int slot, int lane) {
-  return ((slot >> 2) * L + lane) * 4 + (slot & 3);
 }
 
 struct BalParams {
@@ -124,73 +128,126 @@ __device__ __forceinline__ double total_of(float hi, float lo) {
   return isfinite(hi) ? static_cast<double>(hi) + static_cast<double>(lo) : static_cast<double>(hi);
 }
 
-// The k largest of each row, k rounds: the largest value left, the lowest of the
-// chunks that hold it, the lowest of that chunk's elements. Chosen elements (and
-// those past the row's end) become NaN, which no maximum takes; only the chosen
-// chunk's maximum is taken again. Returns the chosen slots of this lane as bits.
-// `a` is used up.
+constexpr uint32_t kFull = 0xffffffffu;
+
+// The choice of every row whose attentions hold NaN, which come last: k rounds
+// over integer keys in the order of the values. Returns the lane's chosen slots.
+// Rare, and out of the way of the loop's registers.
 template <int L, int V>
-__device__ __forceinline__ uint32_t choose(float (&a)[V], int n, int lane, bool live, int k) {
+__device__ __noinline__ uint32_t choose_with_nan(const float (&a)[V], int n, int lane, int k) {
+  uint32_t taken = 0;
+  for (int t = 0; t < k; ++t) {
+    int best = INT_MIN, at = INT_MAX, slot = 0;
+    for (int s = 0; s < V; ++s) {
+      const int e = element_of<L, V>(s, lane);
+      if (e >= n || ((taken >> s) & 1u)) continue;
+      const float v = a[s] + 0.f;  // -0 as +0
+      const int b = __float_as_int(v);
+      const int key = v != v ? INT_MIN + 1 : (b ^ ((b >> 31) & 0x7fffffff));
+      if (key > best || (key == best && e < at)) {
+        best = key;
+        at = e;
+        slot = s;
+      }
+    }
+    int top = best;
+    for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    const int first = row_min<L>(best == top ? at : INT_MAX);
+    if (at == first && first != INT_MAX) taken |= 1u << slot;
+  }
+  return taken;
+}
+
+// The k largest of each row, k rounds: the largest value left, the lowest index
+// of those that hold it. Chosen elements become NaN, which no maximum takes; the
+// caller has seen to it that the row has none. Elements past the row's end become
+// NaN too. `a` is used up; a row that is not `live` keeps its elements.
+template <int L, int V>
+__device__ __forceinline__ void choose_few(float (&a)[V], int n, int lane, bool live, int k) {
+  static_assert(V <= 8, "lane order");
+  const float kNone = __int_as_float(0x7fffffff);
+  const uint32_t below = L == 1 ? 0u : ((1u << (threadIdx.x & 31)) - 1u) &
+                                           ~((1u << ((threadIdx.x & 31) - lane)) - 1u);
+#pragma unroll
+  for (int s = 0; s < V; ++s)
+    if (lane * V + s >= n) a[s] = kNone;
+  for (int t = 0; t < k; ++t) {
+    float best = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+    if (V == 8) best = fmaxf(best, fmaxf(fmaxf(a[4 % V], a[5 % V]), fmaxf(a[6 % V], a[7 % V])));
+    const float top = row_max<L>(best);
+    bool mine = best == top;
+    if (L > 1) mine = (__ballot_sync(kFull, mine) & below) == 0 && mine;  // the row's lowest lane
+    const float gone = mine && live ? top : kNone;  // (nothing equals NaN)
+    bool found = false;
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      const bool hit = a[s] == gone && !found;
+      if (hit) a[s] = kNone;
+      found = found || hit;
+    }
+  }
+}
+
+// The same where a lane holds many values: every lane keeps the maximum of each
+// of its chunks, and the best of those with its chunk; a round takes the winner
+// from those and renews them for the one chunk it took from. Counts go to shared
+// memory. Returns whether the row ran out of numbers (NaN in it are still to be
+// chosen).
+template <int V>
+__device__ __forceinline__ bool choose_many(float (&a)[V], int n, int lane, bool live, int k,
+                                            int* count) {
   constexpr int C = V / 4;
   const float kNone = __int_as_float(0x7fffffff);
   float g[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if ((c * L + lane) * 4 + 3 >= n) {
+    if ((c + 1) * 128 > n) {  // the chunks that reach past the row's end
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if ((c * L + lane) * 4 + q >= n) a[4 * c + q] = kNone;
+        if ((c * 32 + lane) * 4 + q >= n) a[4 * c + q] = kNone;
     }
     g[c] = fmaxf(fmaxf(a[4 * c], a[4 * c + 1]), fmaxf(a[4 * c + 2], a[4 * c + 3]));
   }
-  uint32_t taken = 0;
-  float top = 0.f;
-  for (int t = 0; t < k; ++t) {
-    float best = g[0];
+  float best = kNone, top = 0.f;
+  int chunk = 0;
+  const auto renew = [&] {
+    best = g[0];
 #pragma unroll
     for (int c = 1; c < C; ++c) best = fmaxf(best, g[c]);
-    top = row_max<L>(best);
-    int at = INT_MAX;
 #pragma unroll
     for (int c = C - 1; c >= 0; --c)
-      if (g[c] == top) at = c * L + lane;
-    const int first = row_min<L>(at);
-    const bool mine = live && at == first && first != INT_MAX;
-    const int chunk = L == 32 ? first / 32 : at / L;  // one for the whole warp where L is 32
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (chunk == c && mine) {
-        const bool q0 = a[4 * c] == top, q1 = a[4 * c + 1] == top, q2 = a[4 * c + 2] == top;
-        const int q = q0 ? 0 : q1 ? 1 : q2 ? 2 : 3;
-        taken |= 1u << (4 * c + q);
-        a[4 * c] = q == 0 ? kNone : a[4 * c];
-        a[4 * c + 1] = q == 1 ? kNone : a[4 * c + 1];
-        a[4 * c + 2] = q == 2 ? kNone : a[4 * c + 2];
-        a[4 * c + 3] = q == 3 ? kNone : a[4 * c + 3];
-        g[c] = fmaxf(fmaxf(a[4 * c], a[4 * c + 1]), fmaxf(a[4 * c + 2], a[4 * c + 3]));
-      }
+      if (g[c] == best) chunk = c;
+  };
+  renew();
+  for (int t = 0; t < k; ++t) {
+    top = row_max<32>(best);
+    const int first = row_min<32>(best == top ? chunk * 32 + lane : INT_MAX);
+    const bool mine = live && (first & 31) == lane && first != INT_MAX;
+    int q = 0;
+    switch (first >> 5) {  // the same chunk for the whole warp
+#define DCT_TAKE(c)                                                                           \
+  case c:                                                                                     \
+    if (c < C && mine) {                                                                      \
+      constexpr int b = 4 * (c < C ? c : 0);                                                  \
+      q = a[b] == top ? 0 : a[b + 1] == top ? 1 : a[b + 2] == top ? 2 : 3;                    \
+      a[b] = q == 0 ? kNone : a[b];                                                           \
+      a[b + 1] = q == 1 ? kNone : a[b + 1];                                                   \
+      a[b + 2] = q == 2 ? kNone : a[b + 2];                                                   \
+      a[b + 3] = q == 3 ? kNone : a[b + 3];                                                   \
+      g[c < C ? c : 0] = fmaxf(fmaxf(a[b], a[b + 1]), fmaxf(a[b + 2], a[b + 3]));             \
+    }                                                                                         \
+    break;
+      DCT_TAKE(0) DCT_TAKE(1) DCT_TAKE(2) DCT_TAKE(3)
+      DCT_TAKE(4) DCT_TAKE(5) DCT_TAKE(6) DCT_TAKE(7)
+#undef DCT_TAKE
+      default: break;
+    }
+    if (mine) {
+      atomicAdd(&count[first * 4 + q], 1);
+      renew();
     }
   }
-  // A row with fewer than k numbers: its NaN in the order of their places.
-  if (__any_sync(0xffffffffu, live && top != top)) {
-    int chosen = __popc(taken);
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
-    for (int t = 0; t < k; ++t) {
-      int at = INT_MAX, slot = 0;
-#pragma unroll
-      for (int s = V - 1; s >= 0; --s) {
-        const int e = element_of<L, V>(s, lane);
-        if (e < n && !((taken >> s) & 1u)) {
-          at = e;
-          slot = s;
-        }
-      }
-      const int first = row_min<L>(at);
-      if (live && chosen + t < k && at == first && at != INT_MAX) taken |= 1u << slot;
-    }
-  }
-  return taken;
+  return live && top != top;
 }
 
 // p = a / S with S = sum a, and 0 where S = 0: a reciprocal and products, except
@@ -215,57 +272,81 @@ __device__ __forceinline__ float normalise(float (&a)[V]) {
 struct BalShared {
   double sum[kBalMaxN];
   int count[kBalMaxN];
+  double part[8 * 256];   // eight warps' sums of up to 256 columns
   int kept;
 };
 
-// The column sums and counts of one group over every gridwise-strided batch of
+// The column sums and counts of one group over batches part, part + parts, ... of
 // rows, into `sh` (which no thread may still be reading).
-template <int L, int V>
+template <int L, int V, int THREADS>
 __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long part,
                                            long long parts, BalShared& sh) {
-  constexpr int R = 32 / L;          // rows per warp
-  constexpr bool kRegCounts = V <= 8;  // counts in registers; else in shared memory
+  constexpr int R = 32 / L, W = THREADS / 32;   // rows per warp, warps
+  constexpr bool kFew = V <= 8;                 // counts in registers; else in shared memory
   const int tid = threadIdx.x, warp = tid >> 5, wl = tid & 31, lane = wl % L, sub = wl / L;
   const int n = p.n;
   const bool select = p.top_k < n;
-  for (int i = tid; i < n; i += kBalThreads) {
+  for (int i = tid; i < n; i += THREADS) {
     sh.count[i] = 0;
     sh.sum[i] = 0.0;
   }
   if (tid == 0) sh.kept = 0;
   __syncthreads();
   Sum2 acc[V / 2];
-  int cnt[kRegCounts ? V : 1];
+  int cnt[kFew ? V : 1];
 #pragma unroll
   for (int s = 0; s < V / 2; ++s) acc[s].hi = acc[s].lo = 0ull;
 #pragma unroll
-  for (int s = 0; s < (kRegCounts ? V : 1); ++s) cnt[s] = 0;
+  for (int s = 0; s < (kFew ? V : 1); ++s) cnt[s] = 0;
   int kept = 0;
-  const long long step = parts * (kBalWarps * R);
-  for (long long base = (part * kBalWarps + warp) * R; base < p.rows; base += step) {
+  const long long step = parts * (W * R);
+  for (long long base = (part * W + warp) * R; base < p.rows; base += step) {
     const long long r = base + sub;
     const bool live = r < p.rows && (!p.mask || p.mask[r]);
     float a[V];
     load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live, a);
     if (live && lane == 0) ++kept;
-    float w[V];
+    {
+      float w[V];
 #pragma unroll
-    for (int s = 0; s < V; ++s) w[s] = a[s];
-    if (p.sigmoid) normalise<L, V>(w);
+      for (int s = 0; s < V; ++s) w[s] = a[s];
+      if (p.sigmoid) normalise<L, V>(w);
 #pragma unroll
-    for (int s = 0; s < V; s += 2) accumulate(acc[s / 2], pack2(w[s], w[s + 1]));
-    if (select) {
-      uint32_t taken = choose<L, V>(a, n, lane, live, p.top_k);
-      if (kRegCounts) {
+      for (int s = 0; s < V; s += 2) accumulate(acc[s / 2], pack2(w[s], w[s + 1]));
+    }
+    if (!select) continue;
+    if constexpr (kFew) {
+      // NaN (or opposite infinities) in the lane's values show in their sum
+      float all = (a[0] + a[1]) + (a[2] + a[3]);
+      if (V == 8) all += (a[4 % V] + a[5 % V]) + (a[6 % V] + a[7 % V]);
+      if (__any_sync(kFull, all != all)) {
+        float copy[V];  // (only this branch puts the row into local memory)
 #pragma unroll
-        for (int s = 0; s < V; ++s) cnt[kRegCounts ? s : 0] += (taken >> s) & 1u;
+        for (int s = 0; s < V; ++s) copy[s] = a[s];
+        const uint32_t taken = choose_with_nan<L, V>(copy, n, lane, p.top_k);
+#pragma unroll
+        for (int s = 0; s < V; ++s) cnt[s] += live ? (taken >> s) & 1u : 0;
       } else {
-        for (; taken; taken &= taken - 1)
-          atomicAdd(&sh.count[element_of<L, V>(__ffs(taken) - 1, lane)], 1);
+        choose_few<L, V>(a, n, lane, live, p.top_k);
+#pragma unroll
+        for (int s = 0; s < V; ++s) cnt[s] += a[s] != a[s] ? 1 : 0;  // (past n: not read)
+      }
+    } else {
+      if (__any_sync(kFull, choose_many<V>(a, n, lane, live, p.top_k, sh.count))) {
+        // the numbers are counted; the NaN that follow them, from the row as it was
+        float copy[V];
+        load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live,
+                       copy);
+        const uint32_t taken = choose_with_nan<L, V>(copy, n, lane, p.top_k);
+#pragma unroll
+        for (int s = 0; s < V; ++s)
+          if (live && copy[s] != copy[s] && ((taken >> s) & 1u))
+            atomicAdd(&sh.count[element_of<L, V>(s, lane)], 1);
       }
     }
   }
-  // the rows of a warp, then the warps in order
+  if (kept) atomicAdd(&sh.kept, kept);
+  // a warp's rows by shuffles, then the warps in order
   double sum[V];
 #pragma unroll
   for (int s = 0; s < V; s += 2) {
@@ -279,38 +360,58 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
   for (int s = 0; s < V; ++s) {
 #pragma unroll
     for (int o = 16; o >= L; o >>= 1) {
-      sum[s] += __shfl_xor_sync(0xffffffffu, sum[s], o);
-      if (kRegCounts) cnt[kRegCounts ? s : 0] += __shfl_xor_sync(0xffffffffu, cnt[kRegCounts ? s : 0], o);
+      sum[s] += __shfl_xor_sync(kFull, sum[s], o);
+      if (kFew) cnt[kFew ? s : 0] += __shfl_xor_sync(kFull, cnt[kFew ? s : 0], o);
     }
   }
-  if (kept) atomicAdd(&sh.kept, kept);
-  for (int w = 0; w < kBalWarps; ++w) {
-    if (warp == w && sub == 0) {
+  if constexpr (kFew) {
+    if (select && sub == 0) {
 #pragma unroll
-      for (int s = 0; s < V; ++s) {
-        const int e = element_of<L, V>(s, lane);
-        if (e < n) {
-          sh.sum[e] += sum[s];
-          if (kRegCounts) sh.count[e] += cnt[kRegCounts ? s : 0];
+      for (int s = 0; s < V; ++s)
+        if (lane * V + s < n && cnt[s]) atomicAdd(&sh.count[lane * V + s], cnt[s]);
+    }
+    for (int w0 = 0; w0 < W; w0 += 8) {
+      if ((warp & ~7) == w0 && sub == 0) {
+#pragma unroll
+        for (int s = 0; s < V; ++s)
+          if (lane * V + s < n) sh.part[(warp & 7) * n + lane * V + s] = sum[s];
+      }
+      __syncthreads();
+      for (int i = tid; i < n; i += THREADS) {
+        double t = sh.sum[i];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += sh.part[w * n + i];
+        sh.sum[i] = t;
+      }
+      if (w0 + 8 < W) __syncthreads();
+    }
+  } else {
+    for (int w = 0; w < W; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+          const int e = element_of<L, V>(s, lane);
+          if (e < n) sh.sum[e] += sum[s];
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
   if (!select)
-    for (int i = tid; i < n; i += kBalThreads) sh.count[i] = sh.kept;
+    for (int i = tid; i < n; i += THREADS) sh.count[i] = sh.kept;
+  __syncthreads();
 }
 
 // One part of the sums of one group (blockIdx.y).
-template <int L, int V>
-__global__ void __launch_bounds__(kBalThreads, V <= 8 ? 4 : 2)
+template <int L, int V, int T>
+__global__ void __launch_bounds__(T)
 balance_forward_kernel(BalParams p) {
   __shared__ BalShared sh;
   const int j = blockIdx.y, n = p.n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  group_sums<L, V>(p, j, blockIdx.x, gridDim.x, sh);
+  group_sums<L, V, T>(p, j, blockIdx.x, gridDim.x, sh);
   const long long out = (static_cast<long long>(blockIdx.x) * p.groups + j) * n;
-  for (int i = threadIdx.x; i < n; i += kBalThreads) {
+  for (int i = threadIdx.x; i < n; i += T) {
     p.part_sum[out + i] = sh.sum[i];
     p.part_count[out + i] = sh.count[i];
   }
@@ -348,16 +449,15 @@ __device__ __forceinline__ double loss_factor(float coef, int n, int top_k, int 
 // Few rows: the whole forward in one launch of one cluster, which takes the
 // groups in turn and meets only for the loss (a launch less: 4 of 13 us of a
 // forward and backward over 64 rows).
-template <int L, int V>
-__global__ void __launch_bounds__(kBalThreads) balance_small_kernel(BalParams p) {
+template <int L, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS) balance_small_kernel(BalParams p) {
   __shared__ BalShared sh;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   double dot = 0.0;
   for (int j = blockIdx.x; j < p.groups; j += gridDim.x) {
-    group_sums<L, V>(p, j, 0, 1, sh);
+    group_sums<L, V, THREADS>(p, j, 0, 1, sh);
     const double over = sh.kept > 0 ? 1.0 / sh.kept : 0.0;
-    for (int i = threadIdx.x; i < p.n; i += kBalThreads) {
-      // (without top_k < n the count was written by this thread just now)
+    for (int i = threadIdx.x; i < p.n; i += THREADS) {
       const double mean = sh.sum[i] * over;
       p.counts[j * p.n + i] = sh.count[i];
       p.mean[j * p.n + i] = static_cast<float>(mean);
@@ -366,14 +466,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_small_kernel(BalParams p)
     if (j == 0 && threadIdx.x == 0) *p.rows_kept = sh.kept;
     __syncthreads();
   }
-  const double total = cluster_sum<kBalThreads>(dot);
+  const double total = cluster_sum<THREADS>(dot);
   if (blockIdx.x == 0 && threadIdx.x == 0)
     *p.loss = static_cast<float>(loss_factor(p.coef, p.n, p.top_k, p.groups) * total);
 }
 
 struct BalFinish {
   int parts, width, n, top_k, groups;  // width = groups * n
-  int tile;                            // columns side by side, a power of two
+  int tile;                            // columns side by side: 16, 32, 64 or 128
+  int split;                           // CTAs that share a tile's parts (then there is one turn)
   float coef;
   const double* part_sum;
   const int* part_count;
@@ -384,43 +485,67 @@ struct BalFinish {
   float* loss;
 };
 
-// The parts added in a fixed order, the means and the loss: one cluster, its CTAs
-// taking tiles of columns in turn, a tile's threads splitting the parts.
+// The parts added in a fixed order, the means and the loss: one cluster. Teams of
+// `split` CTAs take tiles of columns in turn; a tile's parts are split over the
+// team's CTAs and their rows of threads, added by a tree and then through shared
+// memory by the team's first CTA.
 __global__ void __launch_bounds__(kBalFinishThreads) balance_finish_kernel(BalFinish p) {
+  namespace cg = cooperative_groups;
   __shared__ double s_sum[kBalFinishThreads];
   __shared__ int s_count[kBalFinishThreads];
   __shared__ int s_kept;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, col = tid % p.tile, slice = tid / p.tile;
   const int slices = kBalFinishThreads / p.tile;
+  const int rank = blockIdx.x % p.split, team = blockIdx.x / p.split, teams = gridDim.x / p.split;
   if (tid == 0) s_kept = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int k = 0;
   for (int q = tid; q < p.parts; q += kBalFinishThreads) k += p.part_kept[q];
   if (k) atomicAdd(&s_kept, k);
-  __syncthreads();
-  const int kept = s_kept;
-  const double over = kept > 0 ? 1.0 / kept : 0.0;
   double dot = 0.0;
-  for (int i0 = blockIdx.x * p.tile; i0 < p.width; i0 += gridDim.x * p.tile) {
-    const int i = i0 + col;
+  for (int i0 = 0; i0 < p.width; i0 += teams * p.tile) {  // as many turns for every CTA
+    const int i = i0 + team * p.tile + col;
     double sum = 0.0;
     int count = 0;
     if (i < p.width) {
-#pragma unroll 8
-      for (int q = slice; q < p.parts; q += slices) {
-        sum += p.part_sum[static_cast<long long>(q) * p.width + i];
-        count += p.part_count[static_cast<long long>(q) * p.width + i];
+      constexpr int B = 8;  // loads in flight
+      const int hop = slices * p.split;
+      for (int q0 = slice * p.split + rank; q0 < p.parts; q0 += B * hop) {
+        double x[B];
+        int y[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int q = q0 + b * hop;
+          const bool in = q < p.parts;
+          x[b] = in ? p.part_sum[static_cast<long long>(q) * p.width + i] : 0.0;
+          y[b] = in ? p.part_count[static_cast<long long>(q) * p.width + i] : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          sum += x[b];
+          count += y[b];
+        }
       }
     }
     s_sum[tid] = sum;
     s_count[tid] = count;
-    __syncthreads();
-    if (slice == 0 && i < p.width) {
-      for (int q = 1; q < slices; ++q) {
-        sum += s_sum[q * p.tile + col];
-        count += s_count[q * p.tile + col];
+    for (int half = slices / 2; half > 0; half /= 2) {
+      __syncthreads();
+      if (slice < half) {
+        s_sum[tid] = sum += s_sum[tid + half * p.tile];
+        s_count[tid] = count += s_count[tid + half * p.tile];
       }
+    }
+    if (p.split > 1) cluster.sync();  // (there is one turn then: the sums stay until read)
+    else __syncthreads();
+    if (rank == 0 && slice == 0 && i < p.width) {
+      for (int r = 1; r < p.split; ++r) {
+        sum += cluster.map_shared_rank(s_sum, blockIdx.x + r)[col];
+        count += cluster.map_shared_rank(s_count, blockIdx.x + r)[col];
+      }
+      const double over = s_kept > 0 ? 1.0 / s_kept : 0.0;
       const double mean = sum * over;
       p.counts[i] = count;
       p.mean[i] = static_cast<float>(mean);
@@ -428,10 +553,10 @@ __global__ void __launch_bounds__(kBalFinishThreads) balance_finish_kernel(BalFi
     }
     __syncthreads();
   }
-  const double total = cluster_sum<kBalFinishThreads>(dot);
+  const double total = cluster_sum<kBalFinishThreads>(dot);  // (all DSMEM reads lie before it)
   if (blockIdx.x == 0 && tid == 0) {
     *p.loss = static_cast<float>(loss_factor(p.coef, p.n, p.top_k, p.groups) * total);
-    *p.rows_kept = kept;
+    *p.rows_kept = s_kept;
   }
 }
 
@@ -503,8 +628,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(B
     const int e = element_of<L, V>(s, lane);
     c[s] = e < n ? static_cast<float>(slope * p.counts[j * n + e]) : 0.f;
   }
-  const long long step = static_cast<long long>(gridDim.x) * (kBalWarps * R);
-  for (long long base = (static_cast<long long>(blockIdx.x) * kBalWarps + warp) * R; base < p.rows;
+  const long long step = static_cast<long long>(gridDim.x) * ((kBalThreads / 32) * R);
+  for (long long base = (static_cast<long long>(blockIdx.x) * (kBalThreads / 32) + warp) * R; base < p.rows;
        base += step) {
     const long long r = base + sub;
     const bool live = r < p.rows && (!p.mask || p.mask[r]);
@@ -521,7 +646,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(B
     float* d = p.dalpha + r * p.dstride + static_cast<long long>(j) * n;
 #pragma unroll
     for (int ch = 0; ch < V / 4; ++ch) {
-      const int e = (ch * L + lane) * 4;
+      const int e = element_of<L, V>(4 * ch, lane);
       float o[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)

@@ -69,6 +69,8 @@ int check_balance(const dynconv_balance_desc* d) {
   return DYNCONV_OK;
 }
 
+constexpr int kBalWarps = dct::kBalThreads / 32;
+
 // Lanes of a warp that hold one row (see balance_kernels.cuh).
 int row_lanes(int n) {
   int lanes = 1;
@@ -76,24 +78,35 @@ int row_lanes(int n) {
   return lanes;
 }
 
-// The whole forward in one launch of one cluster of up to eight CTAs, each taking
-// every eighth group: while the busiest of them has at most 32 K attentions.
+// The whole forward in one launch of one cluster of up to eight CTAs of 256 or
+// 1024 threads, each taking every eighth group: while the busiest of them has at
+// most 4 K attentions of at most 256 experts.
 bool balance_small(const dynconv_balance_desc* d) {
   const long long turns = (d->groups + dct::kBalCluster - 1) / dct::kBalCluster;
-  return turns * d->rows * d->n <= 32768;
+  return d->n <= 256 && turns * d->rows * d->n <= 4096;
 }
 
-// Parts of the forward's sums: CTAs per group, as many in all as run at a time
-// on 148 SMs.
-int balance_parts(const dynconv_balance_desc* d) {
-  const long long per = dct::kBalWarps * (32 / row_lanes(d->n));
-  const long long want = (d->rows + per - 1) / per;
-  const long long most = (d->n <= 256 ? 592 : 296) / d->groups;
-  return static_cast<int>(std::max(1LL, std::min(want, most)));
+// The forward's split over CTAs (per group): CTAs with an SM of 148 to themselves,
+// or, where those would leave SMs idle, four times as many of 256 threads.
+struct BalSplit {
+  int parts, threads;
+};
+BalSplit balance_split(const dynconv_balance_desc* d) {
+  const int lanes = row_lanes(d->n);
+  const auto ctas = [&](int threads) { return (d->rows + threads / lanes - 1LL) / (threads / lanes); };
+  BalSplit s;
+  s.threads = dct::forward_threads(d->n <= 256 ? 8 : 16);
+  int most = 148;
+  if (ctas(s.threads) * d->groups < 148) {
+    s.threads = dct::kBalThreads;
+    most = 592;
+  }
+  s.parts = static_cast<int>(std::max(1LL, std::min<long long>(ctas(s.threads), most / d->groups)));
+  return s;
 }
 
 size_t balance_bytes(const dynconv_balance_desc* d) {
-  const size_t parts = balance_parts(d), width = 1ull * d->groups * d->n;
+  const size_t parts = balance_split(d).parts, width = 1ull * d->groups * d->n;
   return align16(parts * width * 8) + align16(parts * width * 4) + align16(parts * 4);
 }
 
@@ -113,12 +126,16 @@ int with_layout(int n, F f) {
 
 struct LaunchForward {
   dim3 grid;
+  int threads;
   cudaStream_t s;
   const dct::BalParams& p;
   template <int L, int V>
   int operator()() const {
-    return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V>, grid,
-                  dct::kBalThreads, 0, s, p);
+    constexpr int T = dct::forward_threads(V), F = dct::kBalThreads;
+    if (threads == T)
+      return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V, T>, grid, T, 0, s,
+                    p);
+    return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V, F>, grid, F, 0, s, p);
   }
 };
 struct LaunchSmall {
@@ -127,8 +144,14 @@ struct LaunchSmall {
   const dct::BalParams& p;
   template <int L, int V>
   int operator()() const {
-    return launch_cluster("balance_small_kernel", dct::balance_small_kernel<L, V>, dim3(ctas), ctas,
-                          dct::kBalThreads, 0, s, p);
+    if constexpr (V <= 8) {
+      if (p.rows <= 256 / L)  // one turn of the rows
+        return launch_cluster("balance_small_kernel", dct::balance_small_kernel<L, V, 256>,
+                              dim3(ctas), ctas, 256, 0, s, p);
+      return launch_cluster("balance_small_kernel", dct::balance_small_kernel<L, V, 1024>,
+                            dim3(ctas), ctas, 1024, 0, s, p);
+    }
+    return DYNCONV_ERR_UNSUPPORTED;  // not reached: balance_small() is false above n = 256
   }
 };
 struct LaunchSigmoid {
@@ -250,7 +273,8 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   dc_lib::DeviceInfo di;
   rc = dc_lib::device_info(&di);
   if (rc) return rc;
-  const int parts = balance_parts(desc);
+  const BalSplit split = balance_split(desc);
+  const int parts = split.parts;
   const size_t width = 1ull * desc->groups * desc->n;
   char* ws = static_cast<char*>(workspace);
   dct::BalParams p{};
@@ -274,7 +298,7 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (balance_small(desc))
     return with_layout(desc->n, LaunchSmall{std::min(desc->groups, dct::kBalCluster), s, p});
-  rc = with_layout(desc->n, LaunchForward{dim3(parts, desc->groups), s, p});
+  rc = with_layout(desc->n, LaunchForward{dim3(parts, desc->groups), split.threads, s, p});
   if (rc) return rc;
   dct::BalFinish f{};
   f.parts = parts;
@@ -290,14 +314,17 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   f.mean = mean;
   f.rows_kept = rows_kept;
   f.loss = loss;
-  // columns side by side: enough for 32-byte rows of parts, few enough that the
-  // parts are split over many threads
+  // Columns side by side: few, so that many threads share the parts, but not more
+  // than two turns of tiles for a CTA; with fewer than eight tiles, several CTAs
+  // share a tile's parts.
+  const int w = static_cast<int>(width);
+  const auto tiles = [&] { return (w + f.tile - 1) / f.tile; };
   f.tile = 16;
-  while (f.tile < 64 && f.tile < static_cast<int>(width)) f.tile *= 2;
-  const int tiles = (static_cast<int>(width) + f.tile - 1) / f.tile;
-  const int ctas = std::min(tiles, dct::kBalCluster);
-  return launch_cluster("balance_finish_kernel", dct::balance_finish_kernel, dim3(ctas), ctas,
-                        dct::kBalFinishThreads, 0, s, f);
+  while (f.tile < 128 && tiles() > 2 * dct::kBalCluster) f.tile *= 2;
+  f.split = 1;
+  while (tiles() * f.split * 2 <= dct::kBalCluster) f.split *= 2;
+  return launch_cluster("balance_finish_kernel", dct::balance_finish_kernel,
+                        dim3(dct::kBalCluster), dct::kBalCluster, dct::kBalFinishThreads, 0, s, f);
 }
 
 int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alpha,
@@ -340,7 +367,7 @@ int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alph
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sigmoid) {
     p.vec = p.vec && aligned(alpha, 16) && desc->row_stride % 4 == 0 && desc->n % 4 == 0;
-    const long long per = dct::kBalWarps * (32 / row_lanes(desc->n));
+    const long long per = kBalWarps * (32 / row_lanes(desc->n));
     const long long want = (desc->rows + per - 1) / per;
     const int grid = static_cast<int>(
         std::min<long long>(want, std::max(1LL, 8LL * di.sms / desc->groups)));
