@@ -87,6 +87,7 @@ struct BalParams {
   double* part_sum;            // [parts][groups][n]
   int* part_count;             // [parts][groups][n]
   int* part_kept;              // [parts]
+  unsigned* ticket;            // zeroed for the finishing kernel
   int* counts;                 // results (the one-launch form)
   float* mean;
   int* rows_kept;
@@ -159,30 +160,45 @@ __device__ __noinline__ uint32_t choose_with_nan(const float (&a)[V], int n, int
 }
 
 // The k largest of each row, k rounds: the largest value left, the lowest index
-// of those that hold it. Chosen elements become NaN, which no maximum takes; the
-// caller has seen to it that the row has none. Elements past the row's end become
-// NaN too. `a` is used up; a row that is not `live` keeps its elements.
+// of those that hold it; `cnt` counts the lane's chosen slots. Chosen elements
+// become NaN, which no maximum takes; the caller has seen to it that the row has
+// none. Elements past the row's end become NaN too. `a` is used up.
 template <int L, int V>
-__device__ __forceinline__ void choose_few(float (&a)[V], int n, int lane, bool live, int k) {
+__device__ __forceinline__ void choose_few(float (&a)[V], int n, int lane, bool live, int k,
+                                           int (&cnt)[V]) {
   static_assert(V <= 8, "lane order");
   const float kNone = __int_as_float(0x7fffffff);
   const uint32_t below = L == 1 ? 0u : ((1u << (threadIdx.x & 31)) - 1u) &
                                            ~((1u << ((threadIdx.x & 31) - lane)) - 1u);
+  if (n < L * V) {
 #pragma unroll
-  for (int s = 0; s < V; ++s)
-    if (lane * V + s >= n) a[s] = kNone;
-  for (int t = 0; t < k; ++t) {
+    for (int s = 0; s < V; ++s)
+      if (lane * V + s >= n) a[s] = kNone;
+  }
+  for (int t = 1;; ++t) {
     float best = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
     if (V == 8) best = fmaxf(best, fmaxf(fmaxf(a[4 % V], a[5 % V]), fmaxf(a[6 % V], a[7 % V])));
     const float top = row_max<L>(best);
-    bool mine = best == top;
-    if (L > 1) mine = (__ballot_sync(kFull, mine) & below) == 0 && mine;  // the row's lowest lane
-    const float gone = mine && live ? top : kNone;  // (nothing equals NaN)
+    bool mine = live && best == top;
+    if (L > 1) mine = (__ballot_sync(kFull, best == top) & below) == 0 && mine;  // the lowest lane
+    const float gone = mine ? top : kNone;  // (nothing equals NaN)
     bool found = false;
+    if (t == k) {
+#pragma unroll
+      for (int s = 0; s < V; ++s) {
+        const bool hit = a[s] == gone && !found;
+        if (hit) ++cnt[s];
+        found = found || hit;
+      }
+      return;
+    }
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       const bool hit = a[s] == gone && !found;
-      if (hit) a[s] = kNone;
+      if (hit) {
+        ++cnt[s];
+        a[s] = kNone;
+      }
       found = found || hit;
     }
   }
@@ -250,23 +266,30 @@ __device__ __forceinline__ bool choose_many(float (&a)[V], int n, int lane, bool
   return live && top != top;
 }
 
-// p = a / S with S = sum a, and 0 where S = 0: a reciprocal and products, except
-// where the reciprocal of so small a sum would overflow.
-template <int L, int V>
-__device__ __forceinline__ float normalise(float (&a)[V]) {
-  float total = 0.f;
+// The sum of a lane's values.
+template <int V>
+__device__ __forceinline__ float lane_sum(const float (&a)[V]) {
+  unsigned long long t = pack2(a[0], a[1]);
 #pragma unroll
-  for (int s = 0; s < V; ++s) total += a[s];
-  total = row_sum<L>(total);
-  if (fabsf(total) < 1e-30f) {
-#pragma unroll
-    for (int s = 0; s < V; ++s) a[s] = total != 0.f ? __fdiv_rn(a[s], total) : 0.f;
-  } else {
-    const float inv = __frcp_rn(total);
+  for (int s = 2; s < V; s += 2) t = add2(t, pack2(a[s], a[s + 1]));
+  float x, y;
+  unpack2(t, x, y);
+  return x + y;
+}
+
+// p = a / total, and 0 where the total is 0: a reciprocal (relative error 2^-23) and
+// products, except where the reciprocal would leave fp32's normal numbers.
+template <int V>
+__device__ __forceinline__ void normalise(float (&a)[V], float total) {
+  if (fabsf(total) >= 1e-30f && fabsf(total) <= 1e30f) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
 #pragma unroll
     for (int s = 0; s < V; ++s) a[s] *= inv;
+  } else {
+#pragma unroll
+    for (int s = 0; s < V; ++s) a[s] = total != 0.f ? __fdiv_rn(a[s], total) : 0.f;
   }
-  return total;
 }
 
 struct BalShared {
@@ -293,11 +316,11 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
   if (tid == 0) sh.kept = 0;
   __syncthreads();
   Sum2 acc[V / 2];
-  int cnt[kFew ? V : 1];
+  int cnt[V];  // (used where kFew)
 #pragma unroll
   for (int s = 0; s < V / 2; ++s) acc[s].hi = acc[s].lo = 0ull;
 #pragma unroll
-  for (int s = 0; s < (kFew ? V : 1); ++s) cnt[s] = 0;
+  for (int s = 0; s < V; ++s) cnt[s] = 0;
   int kept = 0;
   const long long step = parts * (W * R);
   for (long long base = (part * W + warp) * R; base < p.rows; base += step) {
@@ -306,20 +329,19 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
     float a[V];
     load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live, a);
     if (live && lane == 0) ++kept;
+    const float mine = p.sigmoid || (kFew && select) ? lane_sum<V>(a) : 0.f;
     {
       float w[V];
 #pragma unroll
       for (int s = 0; s < V; ++s) w[s] = a[s];
-      if (p.sigmoid) normalise<L, V>(w);
+      if (p.sigmoid) normalise<V>(w, row_sum<L>(mine));
 #pragma unroll
       for (int s = 0; s < V; s += 2) accumulate(acc[s / 2], pack2(w[s], w[s + 1]));
     }
     if (!select) continue;
     if constexpr (kFew) {
       // NaN (or opposite infinities) in the lane's values show in their sum
-      float all = (a[0] + a[1]) + (a[2] + a[3]);
-      if (V == 8) all += (a[4 % V] + a[5 % V]) + (a[6 % V] + a[7 % V]);
-      if (__any_sync(kFull, all != all)) {
+      if (__any_sync(kFull, mine != mine)) {
         float copy[V];  // (only this branch puts the row into local memory)
 #pragma unroll
         for (int s = 0; s < V; ++s) copy[s] = a[s];
@@ -327,9 +349,7 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
 #pragma unroll
         for (int s = 0; s < V; ++s) cnt[s] += live ? (taken >> s) & 1u : 0;
       } else {
-        choose_few<L, V>(a, n, lane, live, p.top_k);
-#pragma unroll
-        for (int s = 0; s < V; ++s) cnt[s] += a[s] != a[s] ? 1 : 0;  // (past n: not read)
+        choose_few<L, V>(a, n, lane, live, p.top_k, cnt);
       }
     } else {
       if (__any_sync(kFull, choose_many<V>(a, n, lane, live, p.top_k, sh.count))) {
@@ -361,7 +381,7 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
 #pragma unroll
     for (int o = 16; o >= L; o >>= 1) {
       sum[s] += __shfl_xor_sync(kFull, sum[s], o);
-      if (kFew) cnt[kFew ? s : 0] += __shfl_xor_sync(kFull, cnt[kFew ? s : 0], o);
+      if (kFew) cnt[s] += __shfl_xor_sync(kFull, cnt[s], o);
     }
   }
   if constexpr (kFew) {
@@ -415,7 +435,10 @@ balance_forward_kernel(BalParams p) {
     p.part_sum[out + i] = sh.sum[i];
     p.part_count[out + i] = sh.count[i];
   }
-  if (j == 0 && threadIdx.x == 0) p.part_kept[blockIdx.x] = sh.kept;
+  if (j == 0 && threadIdx.x == 0) {
+    p.part_kept[blockIdx.x] = sh.kept;
+    if (blockIdx.x == 0) *p.ticket = 0;
+  }
 }
 
 // Adds `dot` of every thread of the cluster's CTAs, in a fixed order; the sum
@@ -473,88 +496,98 @@ __global__ void __launch_bounds__(THREADS) balance_small_kernel(BalParams p) {
 
 struct BalFinish {
   int parts, width, n, top_k, groups;  // width = groups * n
-  int tile;                            // columns side by side: 16, 32, 64 or 128
-  int split;                           // CTAs that share a tile's parts (then there is one turn)
   float coef;
   const double* part_sum;
   const int* part_count;
   const int* part_kept;
+  double* part_dot;                    // [CTAs]
+  unsigned* ticket;                    // zeroed by the forward kernel
   int* counts;
   float* mean;
   int* rows_kept;
   float* loss;
 };
 
-// The parts added in a fixed order, the means and the loss: one cluster. Teams of
-// `split` CTAs take tiles of columns in turn; a tile's parts are split over the
-// team's CTAs and their rows of threads, added by a tree and then through shared
-// memory by the team's first CTA.
+constexpr int kBalTile = 16;           // columns of a finishing CTA
+
+// The parts added in a fixed order and the means; the CTA that is done last adds
+// what each found of the loss, in the order of the CTAs.
 __global__ void __launch_bounds__(kBalFinishThreads) balance_finish_kernel(BalFinish p) {
-  namespace cg = cooperative_groups;
+  constexpr int S = kBalFinishThreads / kBalTile;
   __shared__ double s_sum[kBalFinishThreads];
   __shared__ int s_count[kBalFinishThreads];
   __shared__ int s_kept;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, col = tid % p.tile, slice = tid / p.tile;
-  const int slices = kBalFinishThreads / p.tile;
-  const int rank = blockIdx.x % p.split, team = blockIdx.x / p.split, teams = gridDim.x / p.split;
+  __shared__ bool s_last;
+  const int tid = threadIdx.x, col = tid % kBalTile, slice = tid / kBalTile;
+  const int i = blockIdx.x * kBalTile + col;
   if (tid == 0) s_kept = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int k = 0;
   for (int q = tid; q < p.parts; q += kBalFinishThreads) k += p.part_kept[q];
   if (k) atomicAdd(&s_kept, k);
-  double dot = 0.0;
-  for (int i0 = 0; i0 < p.width; i0 += teams * p.tile) {  // as many turns for every CTA
-    const int i = i0 + team * p.tile + col;
-    double sum = 0.0;
-    int count = 0;
-    if (i < p.width) {
-      constexpr int B = 8;  // loads in flight
-      const int hop = slices * p.split;
-      for (int q0 = slice * p.split + rank; q0 < p.parts; q0 += B * hop) {
-        double x[B];
-        int y[B];
+  double sum = 0.0;
+  int count = 0;
+  if (i < p.width) {
+    constexpr int B = 8;  // loads in flight
+    for (int q0 = slice; q0 < p.parts; q0 += B * S) {
+      double x[B];
+      int y[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          const int q = q0 + b * hop;
-          const bool in = q < p.parts;
-          x[b] = in ? p.part_sum[static_cast<long long>(q) * p.width + i] : 0.0;
-          y[b] = in ? p.part_count[static_cast<long long>(q) * p.width + i] : 0;
-        }
+      for (int b = 0; b < B; ++b) {
+        const int q = q0 + b * S;
+        const bool in = q < p.parts;
+        x[b] = in ? p.part_sum[static_cast<long long>(q) * p.width + i] : 0.0;
+        y[b] = in ? p.part_count[static_cast<long long>(q) * p.width + i] : 0;
+      }
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          sum += x[b];
-          count += y[b];
-        }
+      for (int b = 0; b < B; ++b) {
+        sum += x[b];
+        count += y[b];
       }
     }
-    s_sum[tid] = sum;
-    s_count[tid] = count;
-    for (int half = slices / 2; half > 0; half /= 2) {
-      __syncthreads();
-      if (slice < half) {
-        s_sum[tid] = sum += s_sum[tid + half * p.tile];
-        s_count[tid] = count += s_count[tid + half * p.tile];
-      }
-    }
-    if (p.split > 1) cluster.sync();  // (there is one turn then: the sums stay until read)
-    else __syncthreads();
-    if (rank == 0 && slice == 0 && i < p.width) {
-      for (int r = 1; r < p.split; ++r) {
-        sum += cluster.map_shared_rank(s_sum, blockIdx.x + r)[col];
-        count += cluster.map_shared_rank(s_count, blockIdx.x + r)[col];
+  }
+  sum += __shfl_xor_sync(kFull, sum, kBalTile);  // the warp's two rows of the tile
+  count += __shfl_xor_sync(kFull, count, kBalTile);
+  if ((tid & kBalTile) == 0) {
+    s_sum[slice / 2 * kBalTile + col] = sum;
+    s_count[slice / 2 * kBalTile + col] = count;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    double dot = 0.0;
+    if (tid < kBalTile && i < p.width) {
+#pragma unroll
+      for (int q = 1; q < S / 2; ++q) {
+        sum += s_sum[q * kBalTile + col];
+        count += s_count[q * kBalTile + col];
       }
       const double over = s_kept > 0 ? 1.0 / s_kept : 0.0;
       const double mean = sum * over;
       p.counts[i] = count;
       p.mean[i] = static_cast<float>(mean);
-      dot += count * over * mean;
+      dot = count * over * mean;
     }
-    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+    if (tid == 0) {
+      p.part_dot[blockIdx.x] = dot;
+      __threadfence();
+      s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
+    }
   }
-  const double total = cluster_sum<kBalFinishThreads>(dot);  // (all DSMEM reads lie before it)
-  if (blockIdx.x == 0 && tid == 0) {
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double total = 0.0;
+  for (int q = tid; q < static_cast<int>(gridDim.x); q += kBalFinishThreads)
+    total += __ldcg(p.part_dot + q);
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+  __syncthreads();
+  if ((tid & 31) == 0) s_sum[tid >> 5] = total;
+  __syncthreads();
+  if (tid == 0) {
+    total = 0.0;
+    for (int w = 0; w < kBalFinishThreads / 32; ++w) total += s_sum[w];
     *p.loss = static_cast<float>(loss_factor(p.coef, p.n, p.top_k, p.groups) * total);
     *p.rows_kept = s_kept;
   }
@@ -635,13 +668,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(B
     const bool live = r < p.rows && (!p.mask || p.mask[r]);
     float a[V];
     load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live, a);
-    const float total = normalise<L, V>(a);
+    const float total = row_sum<L>(lane_sum<V>(a));
+    normalise<V>(a, total);
     float dot = 0.f;
 #pragma unroll
     for (int s = 0; s < V; ++s) dot += c[s] * a[s];
     dot = row_sum<L>(dot);
-    const bool small = fabsf(total) < 1e-30f;
-    const float inv = small ? 0.f : __frcp_rn(total);
+    const bool usual = fabsf(total) >= 1e-30f && fabsf(total) <= 1e30f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
     if (r >= p.rows || (!live && p.accumulate)) continue;  // (a row's lanes agree)
     float* d = p.dalpha + r * p.dstride + static_cast<long long>(j) * n;
 #pragma unroll
@@ -651,7 +686,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(B
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         o[q] = (c[4 * ch + q] - dot) * inv;
-      if (!live || small) {
+      if (!live || !usual) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           o[q] = live && total != 0.f ? __fdiv_rn(c[4 * ch + q] - dot, total) : 0.f;

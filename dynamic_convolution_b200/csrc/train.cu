@@ -105,9 +105,20 @@ BalSplit balance_split(const dynconv_balance_desc* d) {
   return s;
 }
 
-size_t balance_bytes(const dynconv_balance_desc* d) {
+// The forward's workspace: its parts' sums, counts and rows, the finishing CTAs'
+// shares of the loss, and their ticket.
+struct BalLayout {
+  size_t count, kept, dot, ticket, total;
+};
+BalLayout balance_layout(const dynconv_balance_desc* d) {
   const size_t parts = balance_split(d).parts, width = 1ull * d->groups * d->n;
-  return align16(parts * width * 8) + align16(parts * width * 4) + align16(parts * 4);
+  BalLayout l;
+  l.count = align16(parts * width * 8);
+  l.kept = l.count + align16(parts * width * 4);
+  l.dot = l.kept + align16(parts * 4);
+  l.ticket = l.dot + align16((width + dct::kBalTile - 1) / dct::kBalTile * 8);
+  l.total = l.ticket + 16;
+  return l;
 }
 
 // Calls f with the row layout <L, V> for n attentions.
@@ -254,7 +265,7 @@ int launch_adam(const dct::AdamShared& h, const dct::AdamEntry* e, int sms, cuda
 extern "C" {
 
 size_t dynconv_balance_workspace_size(const dynconv_balance_desc* desc) {
-  return check_balance(desc) == DYNCONV_OK ? balance_bytes(desc) : 0;
+  return check_balance(desc) == DYNCONV_OK ? balance_layout(desc).total : 0;
 }
 
 int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha,
@@ -266,7 +277,8 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   if ((!alpha && desc->rows > 0) || !counts || !mean || !rows_kept || !loss ||
       !std::isfinite(coef))
     return DYNCONV_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < balance_bytes(desc)) return DYNCONV_ERR_WORKSPACE;
+  const BalLayout layout = balance_layout(desc);
+  if (!workspace || workspace_bytes < layout.total) return DYNCONV_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(alpha, 4) || !aligned(counts, 4) || !aligned(mean, 4) ||
       !aligned(rows_kept, 4) || !aligned(loss, 4))
     return DYNCONV_ERR_MISALIGNED;
@@ -288,8 +300,9 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   p.alpha = alpha;
   p.mask = row_mask;
   p.part_sum = reinterpret_cast<double*>(ws);
-  p.part_count = reinterpret_cast<int*>(ws + align16(parts * width * 8));
-  p.part_kept = reinterpret_cast<int*>(ws + align16(parts * width * 8) + align16(parts * width * 4));
+  p.part_count = reinterpret_cast<int*>(ws + layout.count);
+  p.part_kept = reinterpret_cast<int*>(ws + layout.kept);
+  p.ticket = reinterpret_cast<unsigned*>(ws + layout.ticket);
   p.coef = coef;
   p.counts = counts;
   p.mean = mean;
@@ -310,21 +323,15 @@ int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha
   f.part_sum = p.part_sum;
   f.part_count = p.part_count;
   f.part_kept = p.part_kept;
+  f.part_dot = reinterpret_cast<double*>(ws + layout.dot);
+  f.ticket = p.ticket;
   f.counts = counts;
   f.mean = mean;
   f.rows_kept = rows_kept;
   f.loss = loss;
-  // Columns side by side: few, so that many threads share the parts, but not more
-  // than two turns of tiles for a CTA; with fewer than eight tiles, several CTAs
-  // share a tile's parts.
-  const int w = static_cast<int>(width);
-  const auto tiles = [&] { return (w + f.tile - 1) / f.tile; };
-  f.tile = 16;
-  while (f.tile < 128 && tiles() > 2 * dct::kBalCluster) f.tile *= 2;
-  f.split = 1;
-  while (tiles() * f.split * 2 <= dct::kBalCluster) f.split *= 2;
-  return launch_cluster("balance_finish_kernel", dct::balance_finish_kernel,
-                        dim3(dct::kBalCluster), dct::kBalCluster, dct::kBalFinishThreads, 0, s, f);
+  return launch("balance_finish_kernel", dct::balance_finish_kernel,
+                dim3(static_cast<unsigned>((width + dct::kBalTile - 1) / dct::kBalTile)),
+                dct::kBalFinishThreads, 0, s, f);
 }
 
 int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alpha,
