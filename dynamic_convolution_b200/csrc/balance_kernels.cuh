@@ -19,7 +19,8 @@ namespace dct {
 constexpr int kBalThreads = 256;
 // Threads of a forward CTA that has an SM to itself, so that few parts are left to
 // be added; where those do not fill the GPU the CTAs have kBalThreads.
-constexpr int forward_threads(int values) { return values <= 8 ? 1024 : 512; }
+// (32 values a lane with their sums want more than the 128 registers of 512.)
+constexpr int forward_threads(int values) { return values <= 8 ? 1024 : values <= 16 ? 512 : 384; }
 constexpr int kBalMaxN = 1024;
 constexpr int kBalMaxTopK = 32;
 constexpr int kBalCluster = 8;          // CTAs of a cluster at most
@@ -266,6 +267,76 @@ __device__ __forceinline__ bool choose_many(float (&a)[V], int n, int lane, bool
   return live && top != top;
 }
 
+// The same for most rows at a fraction of the rounds' cost. The k-th largest of the
+// 32 lanes' maxima is a lower bound of the k-th largest value, so only values not
+// below it can be chosen: k of them or a few more. Those are gathered into `list`
+// (their places; the values are read again from the row), and each lane counts how
+// many come before its own. Returns false, with nothing counted, for a row with
+// more than 32 such values (ties) or with fewer than k lanes that hold a number.
+template <int V>
+__device__ __forceinline__ bool choose_filtered(const float (&a)[V], const float* row, int n,
+                                                int lane, int k, int* count, int* list) {
+  const float kNone = __int_as_float(0x7fffffff);
+  float best = kNone;
+#pragma unroll
+  for (int s = 0; s < V; s += 4) {
+    const int e = element_of<32, V>(s, lane);
+    float m = fmaxf(fmaxf(a[s], a[s + 1]), fmaxf(a[s + 2], a[s + 3]));
+    if ((s / 4 + 1) * 128 > n) {  // a chunk that reaches past the row's end
+      m = kNone;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (e + q < n) m = fmaxf(m, a[s + q]);
+    }
+    best = fmaxf(best, m);
+  }
+  float bound = 0.f;
+  for (int t = 0; t < k; ++t) {
+    bound = row_max<32>(best);
+    if (lane == __ffs(__ballot_sync(kFull, best == bound)) - 1) best = kNone;
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int s = 0; s < V; ++s)
+    if (a[s] >= bound) bits |= 1u << s;
+  if (n < 32 * V) {
+#pragma unroll
+    for (int s = 0; s < V; s += 4)
+      if ((s / 4 + 1) * 128 > n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (element_of<32, V>(s + q, lane) >= n) bits &= ~(1u << (s + q));
+      }
+  }
+  const int held = __popc(bits), all = __reduce_add_sync(kFull, held);
+  if (bound != bound || all > 32) return false;
+  if (all == k) {
+    for (; bits; bits &= bits - 1)
+      atomicAdd(&count[element_of<32, V>(__ffs(bits) - 1, lane)], 1);
+    return true;
+  }
+  int at = held;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int other = __shfl_up_sync(kFull, at, o);
+    if (lane >= o) at += other;
+  }
+  at -= held;
+  for (; bits; bits &= bits - 1) list[at++] = element_of<32, V>(__ffs(bits) - 1, lane);
+  __syncwarp();
+  const int e = lane < all ? list[lane] : INT_MAX;
+  const float v = lane < all ? row[e] : kNone;
+  int before = 0;
+  for (int j = 0; j < all; ++j) {
+    const float w = __shfl_sync(kFull, v, j);
+    const int f = __shfl_sync(kFull, e, j);
+    before += w > v || (w == v && f < e) ? 1 : 0;
+  }
+  if (lane < all && before < k) atomicAdd(&count[e], 1);
+  __syncwarp();  // the list is read
+  return true;
+}
+
 // The sum of a lane's values.
 template <int V>
 __device__ __forceinline__ float lane_sum(const float (&a)[V]) {
@@ -296,14 +367,21 @@ struct BalShared {
   double sum[kBalMaxN];
   int count[kBalMaxN];
   double part[8 * 256];   // eight warps' sums of up to 256 columns
+  int list[16][32];       // each warp's candidates (rows of more than 256)
   int kept;
 };
+
+// Dynamic shared memory of the forward where a lane holds many values: two rows, or
+// in the end the fp64 sums, of each warp.
+constexpr int forward_smem(int values, int threads) {
+  return values <= 8 ? 0 : threads / 32 * 2 * values * 128;
+}
 
 // The column sums and counts of one group over batches part, part + parts, ... of
 // rows, into `sh` (which no thread may still be reading).
 template <int L, int V, int THREADS>
 __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long part,
-                                           long long parts, BalShared& sh) {
+                                           long long parts, BalShared& sh, float4* stage) {
   constexpr int R = 32 / L, W = THREADS / 32;   // rows per warp, warps
   constexpr bool kFew = V <= 8;                 // counts in registers; else in shared memory
   const int tid = threadIdx.x, warp = tid >> 5, wl = tid & 31, lane = wl % L, sub = wl / L;
@@ -322,12 +400,61 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
 #pragma unroll
   for (int s = 0; s < V; ++s) cnt[s] = 0;
   int kept = 0;
+  // The next row is on its way while this one is worked on: in registers where a
+  // lane holds few values, through shared memory where it holds many (each lane
+  // copies and reads its own 16-byte pieces; without alignment for those, not ahead).
   const long long step = parts * (W * R);
-  for (long long base = (part * W + warp) * R; base < p.rows; base += step) {
-    const long long r = base + sub;
-    const bool live = r < p.rows && (!p.mask || p.mask[r]);
-    float a[V];
-    load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live, a);
+  const bool staged = !kFew && p.vec;
+  const auto alive = [&](long long r) { return r < p.rows && (!p.mask || p.mask[r]); };
+  const auto row_at = [&](long long r) { return p.alpha + r * p.stride + static_cast<long long>(j) * n; };
+  const auto stage_of = [&](int k) { return stage + ((k * W + warp) * (V / 4)) * 32 + wl; };
+  const auto copy = [&](long long r, bool live, int k) {
+    if (live) {
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(stage_of(k)));
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) {
+        const int e = element_of<L, V>(4 * c, lane);
+        if (e < n)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + c * 512),
+                       "l"(row_at(r) + e) : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float a[V], ahead[kFew ? V : 1];
+  long long base = (part * W + warp) * R;
+  bool live = base < p.rows && alive(base + sub), next_live = false;
+  if constexpr (kFew) {
+    if (base < p.rows) load_row<L, V>(row_at(base + sub), n, lane, p.vec, live, a);
+  } else if (staged && base < p.rows) {
+    copy(base, live, 0);
+  }
+  for (int turn = 0; base < p.rows; base += step, ++turn) {
+    const long long r = base + sub, next = r + step;
+    if (turn > 0) {
+      live = next_live;
+      if constexpr (kFew) {
+#pragma unroll
+        for (int s = 0; s < V; ++s) a[s] = ahead[s];
+      }
+    }
+    next_live = alive(next);
+    if constexpr (kFew) {
+      load_row<L, V>(row_at(next), n, lane, p.vec, next_live, ahead);
+    } else if (staged) {
+      copy(next, next_live, (turn + 1) & 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (!live) continue;  // (a warp holds one row)
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) {
+        const bool in = element_of<L, V>(4 * c, lane) < n;
+        const float4 f = in ? stage_of(turn & 1)[c * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+        a[4 * c] = f.x; a[4 * c + 1] = f.y; a[4 * c + 2] = f.z; a[4 * c + 3] = f.w;
+      }
+    } else {
+      if (!live) continue;
+      load_row<L, V>(row_at(r), n, lane, false, true, a);
+    }
     if (live && lane == 0) ++kept;
     const float mine = p.sigmoid || (kFew && select) ? lane_sum<V>(a) : 0.f;
     {
@@ -352,19 +479,21 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
         choose_few<L, V>(a, n, lane, live, p.top_k, cnt);
       }
     } else {
+      const float* row = row_at(r);
+      if (choose_filtered<V>(a, row, n, lane, p.top_k, sh.count, sh.list[warp])) continue;
       if (__any_sync(kFull, choose_many<V>(a, n, lane, live, p.top_k, sh.count))) {
         // the numbers are counted; the NaN that follow them, from the row as it was
         float copy[V];
-        load_row<L, V>(p.alpha + r * p.stride + static_cast<long long>(j) * n, n, lane, p.vec, live,
-                       copy);
+        load_row<L, V>(row, n, lane, p.vec, live, copy);
         const uint32_t taken = choose_with_nan<L, V>(copy, n, lane, p.top_k);
 #pragma unroll
         for (int s = 0; s < V; ++s)
-          if (live && copy[s] != copy[s] && ((taken >> s) & 1u))
+          if (copy[s] != copy[s] && ((taken >> s) & 1u))
             atomicAdd(&sh.count[element_of<L, V>(s, lane)], 1);
       }
     }
   }
+  if (!kFew) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (kept) atomicAdd(&sh.kept, kept);
   // a warp's rows by shuffles, then the warps in order
   double sum[V];
@@ -406,15 +535,16 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
       if (w0 + 8 < W) __syncthreads();
     }
   } else {
-    for (int w = 0; w < W; ++w) {
-      if (warp == w) {
+    double* own = reinterpret_cast<double*>(stage);  // [W][32 V], where the rows were
+    __syncthreads();
 #pragma unroll
-        for (int s = 0; s < V; ++s) {
-          const int e = element_of<L, V>(s, lane);
-          if (e < n) sh.sum[e] += sum[s];
-        }
-      }
-      __syncthreads();
+    for (int s = 0; s < V; ++s) own[warp * 32 * V + element_of<L, V>(s, lane)] = sum[s];
+    __syncthreads();
+    for (int i = tid; i < n; i += THREADS) {
+      double t = 0.0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) t += own[w * 32 * V + i];
+      sh.sum[i] = t;
     }
   }
   if (!select)
@@ -426,10 +556,11 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
 template <int L, int V, int T>
 __global__ void __launch_bounds__(T)
 balance_forward_kernel(BalParams p) {
+  extern __shared__ float4 stage[];
   __shared__ BalShared sh;
   const int j = blockIdx.y, n = p.n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  group_sums<L, V, T>(p, j, blockIdx.x, gridDim.x, sh);
+  group_sums<L, V, T>(p, j, blockIdx.x, gridDim.x, sh, stage);
   const long long out = (static_cast<long long>(blockIdx.x) * p.groups + j) * n;
   for (int i = threadIdx.x; i < n; i += T) {
     p.part_sum[out + i] = sh.sum[i];
@@ -478,7 +609,7 @@ __global__ void __launch_bounds__(THREADS) balance_small_kernel(BalParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   double dot = 0.0;
   for (int j = blockIdx.x; j < p.groups; j += gridDim.x) {
-    group_sums<L, V, THREADS>(p, j, 0, 1, sh);
+    group_sums<L, V, THREADS>(p, j, 0, 1, sh, nullptr);
     const double over = sh.kept > 0 ? 1.0 / sh.kept : 0.0;
     for (int i = threadIdx.x; i < p.n; i += THREADS) {
       const double mean = sh.sum[i] * over;

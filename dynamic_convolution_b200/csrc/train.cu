@@ -95,7 +95,7 @@ BalSplit balance_split(const dynconv_balance_desc* d) {
   const int lanes = row_lanes(d->n);
   const auto ctas = [&](int threads) { return (d->rows + threads / lanes - 1LL) / (threads / lanes); };
   BalSplit s;
-  s.threads = dct::forward_threads(d->n <= 256 ? 8 : 16);
+  s.threads = dct::forward_threads(d->n <= 256 ? 8 : d->n <= 512 ? 16 : 32);
   int most = 148;
   if (ctas(s.threads) * d->groups < 148) {
     s.threads = dct::kBalThreads;
@@ -142,11 +142,18 @@ struct LaunchForward {
   const dct::BalParams& p;
   template <int L, int V>
   int operator()() const {
-    constexpr int T = dct::forward_threads(V), F = dct::kBalThreads;
-    if (threads == T)
-      return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V, T>, grid, T, 0, s,
-                    p);
-    return launch("balance_forward_kernel", dct::balance_forward_kernel<L, V, F>, grid, F, 0, s, p);
+    return threads == dct::kBalThreads ? with_threads<L, V, dct::kBalThreads>()
+                                       : with_threads<L, V, dct::forward_threads(V)>();
+  }
+  template <int L, int V, int T>
+  int with_threads() const {
+    const auto kern = dct::balance_forward_kernel<L, V, T>;
+    constexpr int smem = dct::forward_smem(V, T);
+    if (smem > 0) {
+      const cudaError_t e = dc_lib::set_smem(reinterpret_cast<const void*>(kern), smem);
+      if (e != cudaSuccess) return dc_lib::cuda_error(e, "cudaFuncSetAttribute(balance_forward)");
+    }
+    return launch("balance_forward_kernel", kern, grid, T, smem, s, p);
   }
 };
 struct LaunchSmall {
