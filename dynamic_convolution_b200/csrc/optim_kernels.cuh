@@ -28,7 +28,7 @@ __device__ __forceinline__ int find_tensor(const E* e, int count, long long unit
 
 // ------------------------------------------------------------------ the norm
 
-constexpr int kNormUnit = 4096;   // elements a CTA takes at a time, 16 per thread
+constexpr int kNormPiece = 4096;  // elements that a CTA's threads take at a time, 16 each
 struct NormEntry {
   const void* grad;
   long long numel;
@@ -39,8 +39,8 @@ constexpr int kNormCap = 768;
 template <int CAP>
 struct NormTable {
   NormEntry e[CAP];
-  long long units;
-  int count;
+  long long units;   // of `pieces` pieces
+  int count, pieces;
   double* part;
 };
 static_assert(sizeof(NormTable<kNormCap>) <= 32764, "kernel parameters");
@@ -113,10 +113,13 @@ grad_norm_kernel(const __grid_constant__ NormTable<CAP> t) {
   double s0 = 0.0, s1 = 0.0;
   const void* grad = nullptr;
   long long first = 0, stop = 0, numel = 0;
-  int bf16 = 0, vec = 0;
+  int bf16 = 0, vec = 0, k = 0;
   for (long long u = blockIdx.x; u < t.units; u += gridDim.x) {
-    if (u >= stop) {
-      const int k = find_tensor(t.e, t.count, u);
+    if (u >= stop) {  // most often in the next tensor, or the one after it
+      const int near = k + 1 < t.count ? k + 1 : k;
+      if (stop > 0 && (near + 1 >= t.count || u < t.e[near + 1].first)) k = near;
+      else if (stop > 0 && (near + 2 >= t.count || u < t.e[near + 2].first)) k = near + 1;
+      else k = find_tensor(t.e, t.count, u);
       grad = t.e[k].grad;
       numel = t.e[k].numel;
       first = t.e[k].first;
@@ -124,29 +127,33 @@ grad_norm_kernel(const __grid_constant__ NormTable<CAP> t) {
       vec = t.e[k].vec;
       stop = k + 1 < t.count ? t.e[k + 1].first : t.units;
     }
-    const long long i = (u - first) * kNormUnit;
-    if (vec && i + kNormUnit <= numel) {
+    long long i = (u - first) * t.pieces * kNormPiece;
+    const long long end = min(i + static_cast<long long>(t.pieces) * kNormPiece, numel);
+    if (vec) {
       if (bf16) {
-        const uint4* g = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(grad) + i) + threadIdx.x;
-        const uint4 a = g[0], b = g[kOptThreads];
-        add_squares_bf16(a, s0, s1);
-        add_squares_bf16(b, s0, s1);
+        for (; i + kNormPiece <= end; i += kNormPiece) {
+          const uint4* g = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(grad) + i) + threadIdx.x;
+          const uint4 a = g[0], b = g[kOptThreads];
+          add_squares_bf16(a, s0, s1);
+          add_squares_bf16(b, s0, s1);
+        }
       } else {
-        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const float*>(grad) + i) +
-                         threadIdx.x;
-        const uint4 a = g[0], b = g[kOptThreads], x = g[2 * kOptThreads], y = g[3 * kOptThreads];
-        add_squares(a, s0, s1);
-        add_squares(b, s0, s1);
-        add_squares(x, s0, s1);
-        add_squares(y, s0, s1);
+        for (; i + kNormPiece <= end; i += kNormPiece) {
+          const uint4* g = reinterpret_cast<const uint4*>(static_cast<const float*>(grad) + i) +
+                           threadIdx.x;
+          const uint4 a = g[0], b = g[kOptThreads], x = g[2 * kOptThreads], y = g[3 * kOptThreads];
+          add_squares(a, s0, s1);
+          add_squares(b, s0, s1);
+          add_squares(x, s0, s1);
+          add_squares(y, s0, s1);
+        }
       }
-    } else {  // the tensor's end, or a start off the 16-byte grid
-      const long long end = min(i + kNormUnit, numel);
-      for (long long q = i + threadIdx.x; q < end; q += kOptThreads)
-        add_square(bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(grad)[q])
-                        : static_cast<const float*>(grad)[q], s0);
     }
+    // the tensor's end, or a start off the 16-byte grid
+    for (i += threadIdx.x; i < end; i += kOptThreads)
+      add_square(bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(grad)[i])
+                      : static_cast<const float*>(grad)[i], s0);
   }
   double sum = s0 + s1;
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
