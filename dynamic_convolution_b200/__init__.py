@@ -409,17 +409,22 @@ def train_tensor(grad, param=None, m=None, v=None, master=None, m_scale=None, v_
             if dtype != BF16:
                 raise ValueError("a master copy goes with a bf16 param")
             check("master", master, (f32,), numel)
-    return dynconv_train_tensor(
+    entry = dynconv_train_tensor(
         _ptr(param), _ptr(master), _ptr(grad), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale),
         numel, dtype, F32 if grad.dtype is f32 else BF16, bits,
         float(lr_scale), float(weight_decay))
+    entry.keeps = (param, master, grad, m, v, m_scale, v_scale)
+    return entry
 
 
 def train_tensors(entries):
-    """The list that dynconv_grad_norm and dynconv_adamw take. It holds addresses:
-    the tensors must stay where they are while it is used."""
+    """The list that dynconv_grad_norm and dynconv_adamw take. It holds the tensors'
+    addresses and keeps the tensors of train_tensor entries alive; a tensor that is
+    replaced by another (not written in place) needs a new list."""
     entries = list(entries)
-    return (dynconv_train_tensor * len(entries))(*entries)
+    array = (dynconv_train_tensor * len(entries))(*entries)
+    array.keeps = [getattr(e, "keeps", None) for e in entries]
+    return array
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0) -> dynconv_adamw_hyper:

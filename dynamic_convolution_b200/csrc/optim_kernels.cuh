@@ -252,11 +252,12 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float sqrt_normal(float x) {
+__device__ __forceinline__ float rsqrt_approx(float x) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
 // Two fp32 operations in one instruction, each rounded like the single one: the
 // 8-bit kernel is bound by its instruction issue.
 struct Pair {
@@ -279,6 +280,26 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   Pair r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
   return r;
+}
+// Sums of products that were rounded before: two single additions, because the
+// assembler contracts a packed product and a packed sum into one packed
+// multiply-add in spite of their .rn (seen on 26% of random operands).
+__device__ __forceinline__ Pair add_apart(Pair a, Pair b) {
+  float a0, a1, b0, b1;
+  unpair(a, a0, a1);
+  unpair(b, b0, b1);
+  return pair_of(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+// Two square roots by Newton's method: with y near 1 / sqrt(x), r = x y is near the
+// root, x - r^2 is exact in one multiply-add, and r + (x - r^2) y / 2 is within
+// 2^-20 of a unit in the last place of the root before its rounding, so that it is
+// the correctly rounded root but for about one value in a million. For x from 2^-100
+// (below, the residual would be subnormal) to the largest finite number.
+__device__ __forceinline__ Pair sqrt2(float lo, float hi) {
+  const Pair x = pair_of(lo, hi), y = pair_of(rsqrt_approx(lo), rsqrt_approx(hi));
+  const Pair r = x * y;
+  const Pair rest = fma2(r * pair_of(-1.f, -1.f), r, x);
+  return fma2(rest, y * pair_of(0.5f, 0.5f), r);
 }
 __device__ __forceinline__ float min3(float a, float b, float c) {
   float r;
@@ -410,8 +431,7 @@ __device__ __forceinline__ void store4_codes(uint8_t* p, long long i, long long 
 
 // The block's factor and its inverse from its largest magnitude (a non-finite
 // one passes through both: the block is spoilt, not hidden).
-__device__ __forceinline__ void block_scale(uint32_t top_bits, float& scale, float& inv) {
-  const float top = __uint_as_float(top_bits);
+__device__ __forceinline__ void block_scale(float top, float& scale, float& inv) {
   const bool none = top < 7.888609052210118e-31f;  // 2^-100
   scale = none ? 0.f : __fmul_rn(top, 1.f / 448.f);
   inv = none ? 0.f : __fmul_rn(__frcp_rn(top), 448.f);
@@ -457,6 +477,10 @@ __device__ __forceinline__ void adam_load(
   }
 }
 
+// With 8-bit states m and v are advanced with separately rounded products and sums
+// and rooted correctly, so that the codes follow from the formula's fp32 arithmetic
+// and not from how it is contracted: next to a border between codes a difference in
+// the last bit is a difference of a whole code, and that feeds the next step.
 template <int PARAM, bool GRAD16, bool STATE8, bool FAST>
 __device__ __forceinline__ void adam_block(
     const AdamEntry& e, const Hyper& h, long long block,
@@ -465,24 +489,10 @@ __device__ __forceinline__ void adam_block(
   const long long numel = e.numel, first = block * kBlock + lane * 4;
   constexpr int J = 2;
   float p[J][4], m[J][4], v[J][4];
-  uint32_t u[J][2];   // two elements' 16 bits in a word
-  if (STATE8 || PARAM == kParamBf16) {
-    const uint32_t far = static_cast<uint32_t>(block >> 25);  // element >> 33
-    const uint32_t key = far ? h.key ^ mix32(far) : h.key;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t pair = static_cast<uint32_t>((first + 128 * j) >> 1);
-      u[j][0] = mix32(key ^ pair);
-      u[j][1] = mix32(key ^ (pair + 1));
-    }
-  }
-  const auto dither = [&](int j, int q) {
-    return q & 1 ? u[j][q >> 1] >> 16 : u[j][q >> 1] & 0xffffu;
-  };
   const Pair beta1 = pair_of(h.beta1, h.beta1), omb1 = pair_of(h.omb1, h.omb1);
   const Pair beta2 = pair_of(h.beta2, h.beta2), omb2 = pair_of(h.omb2, h.omb2);
   const Pair scale = pair_of(h.scale, h.scale);
-  float mtop = 0.f, vtop = 0.f;            // the block's largest magnitudes,
+  float mtop = 0.f, vtop = 0.f;            // the block's largest |m| and v,
   float mlow = INFINITY, vlow = INFINITY;  // and its smallest
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -502,29 +512,50 @@ __device__ __forceinline__ void adam_block(
         m0 = pair_of(value(r.m[j], q), value(r.m[j], q + 1));
         v0 = pair_of(value(r.v[j], q), value(r.v[j], q + 1));
       }
-      m0 = fma2(m0, beta1, g * omb1);
-      v0 = fma2(v0, beta2, (g * g) * omb2);
+      if (STATE8) {
+        m0 = add_apart(m0 * beta1, g * omb1);
+        v0 = add_apart(v0 * beta2, (g * g) * omb2);
+      } else {
+        m0 = fma2(m0, beta1, g * omb1);
+        v0 = fma2(v0, beta2, (g * g) * omb2);
+      }
       unpair(m0, m[j][q], m[j][q + 1]);
       unpair(v0, v[j][q], v[j][q + 1]);
-      if (STATE8) vlow = min3(vlow, v[j][q], v[j][q + 1]);
+      if (STATE8) {
+        mtop = max3_nan(mtop, fabsf(m[j][q]), fabsf(m[j][q + 1]));
+        vtop = max3_nan(vtop, v[j][q], v[j][q + 1]);
+        mlow = min3(mlow, fabsf(m[j][q]), fabsf(m[j][q + 1]));
+        vlow = min3(vlow, v[j][q], v[j][q + 1]);
+      }
     }
   }
-  // The root's one instruction flushes subnormals; a block that holds one (or a
-  // zero) takes the longer form. (32-bit states are bound by memory: always.)
-  const bool tiny = !STATE8 || __any_sync(0xffffffffu, !(vlow >= 1.17549435e-38f));
+  // 8-bit codes are taken from roots rounded correctly; 32-bit states need the root
+  // for the update alone.
   float root[J][4];
-  if (tiny) {
-    vlow = sqrt_approx(vlow);
+  if constexpr (STATE8) {
+    mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+    vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+    const bool usual = vlow >= 7.888609052210118e-31f && vtop < INFINITY;  // 2^-100
+    if (__all_sync(0xffffffffu, usual)) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2)
+          unpair(sqrt2(v[j][q], v[j][q + 1]), root[j][q], root[j][q + 1]);
+      unpair(sqrt2(vtop, vlow), vtop, vlow);
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) root[j][q] = __fsqrt_rn(v[j][q]);
+      vtop = __fsqrt_rn(vtop);
+      vlow = __fsqrt_rn(vlow);
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) root[j][q] = sqrt_approx(v[j][q]);
-  } else {
-    vlow = sqrt_normal(vlow);
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) root[j][q] = sqrt_normal(v[j][q]);
   }
   const Pair root2 = pair_of(h.root2, h.root2), eps = pair_of(h.eps, h.eps);
   const Pair down = pair_of(-h.size, -h.size), keep = pair_of(h.keep, h.keep);
@@ -537,13 +568,22 @@ __device__ __forceinline__ void adam_block(
       const Pair ratio = pair_of(m[j][q], m[j][q + 1]) * pair_of(rcp_approx(lo), rcp_approx(hi));
       const Pair old = pair_of(value(r.p[j], q), value(r.p[j], q + 1));
       unpair(fma2(ratio, down, old * keep), p[j][q], p[j][q + 1]);
-      if (STATE8) {
-        mtop = max3_nan(mtop, fabsf(m[j][q]), fabsf(m[j][q + 1]));
-        vtop = max3_nan(vtop, root[j][q], root[j][q + 1]);
-        mlow = min3(mlow, fabsf(m[j][q]), fabsf(m[j][q + 1]));
-      }
     }
   }
+  uint32_t u[J][2];   // two elements' 16 bits in a word
+  if (STATE8 || PARAM == kParamBf16) {
+    const uint32_t far = static_cast<uint32_t>(block >> 25);  // element >> 33
+    const uint32_t key = far ? h.key ^ mix32(far) : h.key;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t pair = static_cast<uint32_t>((first + 128 * j) >> 1);
+      u[j][0] = mix32(key ^ pair);
+      u[j][1] = mix32(key ^ (pair + 1));
+    }
+  }
+  const auto dither = [&](int j, int q) {
+    return q & 1 ? u[j][q >> 1] >> 16 : u[j][q >> 1] & 0xffffu;
+  };
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const long long i = first + 128 * j;
@@ -572,8 +612,8 @@ __device__ __forceinline__ void adam_block(
   }
   if (STATE8) {
     float msc, minv, vsc, vinv;
-    block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)), msc, minv);
-    block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)), vsc, vinv);
+    block_scale(mtop, msc, minv);
+    block_scale(vtop, vsc, vinv);
     if (lane == 0) {
       e.m_scale[block] = msc;
       e.v_scale[block] = vsc;

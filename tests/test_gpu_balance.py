@@ -186,6 +186,49 @@ def test_order_of_zeros_negatives_infinities_and_nan():
         assert bool(torch.isnan(c.loss[0]))   # a kept NaN shows
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("n,k", [(12, 3), (100, 7), (300, 5), (1000, 32)])
+def test_nan_among_many_experts(n, k, sigmoid):
+    """Rows with some NaN, and with so many that fewer than k numbers are left."""
+    rows = 40
+    c = Case(rows, n, k, sigmoid=sigmoid, seed=n)
+    rng = np.random.default_rng(n)
+    c.a[3, 0, rng.integers(0, n, 2)] = np.nan
+    c.a[7, 0, rng.permutation(n)[:n - k + 2]] = np.nan
+    c.a[8] = np.nan
+    c.alpha[:rows * n].copy_(torch.from_numpy(c.a.reshape(-1).astype(np.float32)))
+    c.forward()
+    torch.cuda.synchronize()
+    want = np.zeros(n, np.int64)
+    for row in c.a[:, 0]:
+        want[ref.top_k(row, k)] += 1
+    assert np.array_equal(c.counts[:n].cpu().numpy(), want)
+    assert bool(torch.isnan(c.loss[0])) and int(c.kept[0]) == rows
+
+
+@pytest.mark.parametrize("n,k", [(300, 9), (1000, 8)])
+def test_wide_rows_with_a_few_equal_values_at_the_border(n, k):
+    c = Case(64, n, k, seed=k)
+    for b in range(64):                      # b % 9 equal largest values in a row
+        c.a[b, 0, np.random.default_rng(b).permutation(n)[:b % 9 + 2]] = 0.5
+    c.alpha[:64 * n].copy_(torch.from_numpy(c.a.reshape(-1).astype(np.float32)))
+    c.forward()
+    c.check_forward()
+
+
+def test_sigmoid_rows_of_tiny_and_huge_sums():
+    """Sums below and above the reciprocal's range take the division."""
+    c = Case(4, 6, 2, sigmoid=True)
+    scale = np.array([1e-35, 1e-41, 1e33, 1.0])[:, None, None]
+    c.a = (c.a * scale).astype(np.float32).astype(np.float64)
+    c.alpha[:24].copy_(torch.from_numpy(c.a.reshape(-1).astype(np.float32)))
+    c.forward()
+    torch.cuda.synchronize()
+    r = ref.balance(c.a, None, 2, True, COEF)
+    mean = c.mean[:6].double().cpu().numpy()
+    assert np.all(np.abs(mean - r["mean"][0]) <= 13 * ref.E * r["mean"][0])
+
+
 def test_sigmoid_rows_that_sum_to_zero():
     c = Case(5, 6, 1, sigmoid=True)
     c.a[2] = 0.0
@@ -229,6 +272,39 @@ def test_long_offsets():
     g, size = ref.balance_grad(c.a, None, r["counts"], 2, True, COEF, 1.25)
     got = dheld[:, 16:16 + n].double().cpu().numpy()
     assert np.all(np.abs(got - g[:, 0]) <= 60 * ref.E * size[:, 0])
+
+
+def test_long_offsets_softmax_backward():
+    rows, n, stride = 520, 12, 1 << 22
+    c = Case(rows, n, 2)
+    c.forward()
+    r = c.check_forward()
+    for accumulate in (0, 1):
+        wide = torch.full((rows, stride), 2.0, device="cuda")
+        dc.check(dc.dynconv_balance_backward(c.desc, None, None, COEF, c.counts, c.kept, c.dloss,
+                                             wide[:, 8:], stride, accumulate))
+        torch.cuda.synchronize()
+        g, size = ref.balance_grad(c.a, None, r["counts"], 2, False, COEF, 1.25)
+        got = wide[:, 8:8 + n].double().cpu().numpy() - 2.0 * accumulate
+        assert np.all(np.abs(got - g[:, 0]) <= 2 * ref.E * size[:, 0] + 2 * accumulate * 2 * ref.E)
+        assert bool((wide[:, :8] == 2.0).all()) and bool((wide[:, 8 + n:1024] == 2.0).all())
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own workspace and outputs."""
+    cases = [Case(3000, 32, 3, sigmoid=bool(i), mask=0.8, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            c.forward(s)
+            c.backward(0, s)
+    torch.cuda.synchronize()
+    for c in cases:
+        r = c.check_forward()
+        c.fill()
+        c.backward(0)
+        c.check_backward(r, 0)
 
 
 def test_many_rows():

@@ -205,6 +205,37 @@ def test_large_tensor_and_its_tail():
     step_and_check([Tensor(3_000_001, "bf16+master", "fp32", 32), Tensor(3_000_001, "bf16", "bf16", 8)])
 
 
+def test_more_elements_than_31_bits_count():
+    """One tensor of 2^31 + 1000 elements: its start, its middle and its end against
+    the formula, and its norm."""
+    n = (1 << 31) + 1000
+    fp8 = lambda k: torch.zeros(k, dtype=torch.uint8, device="cuda").view(FP8)  # noqa: E731
+    p = torch.full((n,), 0.125, dtype=torch.bfloat16, device="cuda")
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[-5] = 3.0
+    m, v = fp8(n), fp8(n)
+    ms, vs = (torch.zeros(-(-n // 256), device="cuda") for _ in range(2))
+    tensors = dc.train_tensors([dc.train_tensor(grad=g, param=p, m=m, v=v, m_scale=ms, v_scale=vs)])
+    want = math.sqrt(0.25 * (n - 1) + 9)
+    got, _ = grad_norm(tensors)
+    assert abs(got - want) <= 1.01 * E * want
+    dc.check(dc.dynconv_adamw(tensors, dc.make_adamw(step=1, seed=5, **HYPER)))
+    torch.cuda.synchronize()
+    for at in (0, (1 << 31) - 2048, (1 << 31) - 128, n - 488):   # multiples of 8
+        k = min(2048, n - at)
+        here = lambda t: t[at:at + k].float().cpu().double().numpy()  # noqa: E731
+        zero = np.zeros(k)
+        p1, m1, v1, ep, em, ev = ref.adamw(zero + 0.125, here(g), zero, zero, step=1, decay=0.0,
+                                           **HYPER)
+        u = ref.dither(5, 1, 0, k, at)
+        a, b = ref.to_bf16_dithered(p1 - ep, u), ref.to_bf16_dithered(p1 + ep, u)
+        assert np.all((here(p) >= np.minimum(a, b)) & (here(p) <= np.maximum(a, b)))
+        first, last = at // 256, (at + k - 1) // 256
+        top = ms[first:last + 1].double().cpu().numpy() * 448
+        assert np.all(np.isclose(top, 0.05) | np.isclose(top, 0.3))
+        assert np.all(here(m)[:8] > 0) and np.all(here(v) > 0)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_first_step_from_zero_state_and_zero_gradients(bits):
     t = [Tensor(1000, "fp32", "fp32", bits, seed=i) for i in range(2)]
@@ -391,6 +422,19 @@ def test_clip_and_step_captured(param, grad, bits):
             for place, x in enumerate(t):
                 x.check(place, number, 21, scale=factor, lr=float(np.float32(rate)))
     del graphs
+
+
+def test_two_steps_at_once_on_two_streams():
+    sets = [[Tensor(20_000 + s, p, g, b, seed=s) for p, g, b in KINDS] for s in (0, 1)]
+    lists = [dc.train_tensors(x.entry() for x in t) for t in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for tensors, s in zip(lists, streams):
+        dc.check(dc.dynconv_adamw(tensors, dc.make_adamw(step=3, seed=11, **HYPER), stream=s))
+    torch.cuda.synchronize()
+    for t in sets:
+        for i, x in enumerate(t):
+            x.check(i, 3, 11)
 
 
 def test_no_clipping_leaves_the_factor_at_one():

@@ -208,6 +208,18 @@ def test_train_tensor_checks_what_it_is_given():
     e = dc.train_tensor(grad=f(300), param=f(300, torch.bfloat16), master=f(300), m=f(300, fp8),
                         v=f(300, fp8), m_scale=f(2), v_scale=f(2))
     assert (e.state_bits, e.dtype) == (8, dc.BF16)
+    # a list keeps its tensors alive
+    import gc
+    import weakref
+    grad = f(8)
+    alive = weakref.ref(grad)
+    tensors = dc.train_tensors([dc.train_tensor(grad=grad)])
+    del grad
+    gc.collect()
+    assert alive() is not None and tensors[0].grad == alive().data_ptr()
+    del tensors
+    gc.collect()
+    assert alive() is None
     bad = [dict(grad=f(8, torch.float16)), dict(grad=f().view(2, 4).t()),
            dict(grad=f(), param=f()), dict(grad=f(), param=f(9), m=f(), v=f()),
            dict(grad=f(), param=f(8, torch.float64), m=f(), v=f()),

@@ -84,11 +84,11 @@ def _mix(x):
     return x ^ (x >> np.uint64(16))
 
 
-def dither(seed, step, place, numel):
-    """u in [0, 1): 16 bits for every element."""
+def dither(seed, step, place, numel, start=0):
+    """u in [0, 1): 16 bits for every element from `start` (below 2^33) on."""
     lo = np.uint64(0xFFFFFFFF)
     key = _mix(_mix(_mix(seed) ^ (np.uint64(step) & lo)) ^ np.uint64(place))
-    e = np.arange(numel, dtype=np.uint64)
+    e = np.arange(start, start + numel, dtype=np.uint64)
     h = _mix(key ^ (e >> np.uint64(1)))
     u = np.where(e & np.uint64(1), h >> np.uint64(16), h & np.uint64(0xFFFF))
     return u.astype(np.float64) / 65536.0
