@@ -57,6 +57,11 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--backward", action="store_true",
                     help="time the layer's backward step (weight, router and input gradients)")
+    ap.add_argument("--train", action="store_true",
+                    help="time one layer's training step: route, balance loss, forward, "
+                         "backward, gradient norm, AdamW (one GPU)")
+    ap.add_argument("--state-bits", type=int, default=32, choices=(32, 8),
+                    help="bits of the experts' AdamW states for --train")
     ap.add_argument("--cells", type=int, default=0,
                     help="time the layer with its kernel assembled from this many warehouse cells")
     ap.add_argument("--warehouse", type=int, default=128, help="warehouse cells for --cells")
@@ -1062,6 +1067,118 @@ def run_backward(args, cfg):
     return 0
 
 
+def run_train(args, cfg):
+    """One layer's training step on one GPU: dynconv_route, dynconv_balance_forward,
+    dynconv_forward, dynconv_backward_weight, dynconv_balance_backward,
+    dynconv_route_backward, dynconv_backward_data, dynconv_grad_norm and
+    dynconv_adamw (fp32 master copies of bf16 experts), captured once and replayed
+    with the step's number and the clipping factor on the device; also the share of
+    each part, timed alone."""
+    import torch
+
+    import dynamic_convolution_b200 as dc
+    from dynamic_convolution_b200 import build, synth
+
+    torch.cuda.set_device(0)
+    build.build()
+    dc.load()
+    inp = synth.make_inputs(cfg)
+    dys, _ = synth.make_upstream_grad(cfg)
+    bf16 = cfg.dtype == synth.BF16
+    dev = lambda a: (torch.from_numpy(a).view(torch.bfloat16) if bf16
+                     else torch.from_numpy(a)).cuda()
+    x, dy, E = dev(inp.x_store), dev(dys), dev(inp.experts_store)
+    Wr, br, bias = (torch.from_numpy(a).cuda() for a in (inp.Wr, inp.br, inp.bias))
+    f = lambda *s: torch.zeros(s, device="cuda")
+    byte = lambda k: torch.empty(max(k, 16), dtype=torch.uint8, device="cuda")
+    B, n, C, Co = cfg.B, cfg.n, cfg.C_in, cfg.C_out
+    alpha, dalpha, dE, dbias = f(B, n), f(B, n), f(*E.shape), f(n, Co)
+    dWr, dbr, dg, dx = f(n, C), f(n), f(B, C), torch.empty_like(x)
+    y = torch.empty((B, cfg.H_out, cfg.W_out, Co), dtype=E.dtype, device="cuda")
+    d = dc.desc_from_config(cfg)
+    ws = byte(max(dc.dynconv_workspace_size(d), dc.dynconv_backward_workspace_size(d)))
+    bd = dc.make_balance_desc(B, n, mode=cfg.mode)
+    bws = byte(dc.dynconv_balance_workspace_size(bd))
+    counts, kept = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (n, 1))
+    mean, loss = f(n), f(1)
+    entries = []
+    for p, g, decay in ((E, dE, 0.01), (bias, dbias, 0.0), (Wr, dWr, 0.0), (br, dbr, 0.0)):
+        kw = dict(grad=g, param=p, weight_decay=decay)
+        if args.state_bits == 8 and p is E:
+            blocks = -(-p.numel() // 256)
+            m, v = (torch.zeros(p.shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+            kw.update(m=m, v=v, m_scale=f(blocks), v_scale=f(blocks))
+        else:
+            kw.update(m=f(*p.shape), v=f(*p.shape))
+        if p.dtype == torch.bfloat16:
+            kw["master"] = p.float()
+        entries.append(dc.train_tensor(**kw))
+    tensors = dc.train_tensors(entries)
+    nws = byte(dc.dynconv_grad_norm_workspace_size(tensors))
+    stats, number = f(2), torch.zeros(1, dtype=torch.int64, device="cuda")
+    hyper = dc.make_adamw(1e-4)
+    st = torch.cuda.Stream()
+    W = ws.numel()
+    parts = {
+        "route": lambda: [dc.dynconv_route(d, x, Wr, br, cfg.mode, cfg.tau, alpha, st)],
+        "balance_forward": lambda: [dc.dynconv_balance_forward(
+            bd, alpha, None, 0.01, counts, mean, kept, loss, bws, bws.numel(), st)],
+        "forward": lambda: [dc.dynconv_forward(d, x, E, alpha, bias, y, ws, W, st)],
+        "backward_weight": lambda: [dc.dynconv_backward_weight(
+            d, x, dy, E, alpha, bias, dE, dbias, dalpha, ws, W, st)],
+        "balance_backward": lambda: [dc.dynconv_balance_backward(
+            bd, alpha, None, 0.01, counts, kept, None, dalpha, n, 1, st)],
+        "route_backward": lambda: [dc.dynconv_route_backward(
+            d, x, Wr, alpha, dalpha, cfg.mode, cfg.tau, dWr, dbr, dg, ws, W, st)],
+        "backward_data": lambda: [dc.dynconv_backward_data(d, dy, E, alpha, dg, dx, ws, W, st)],
+        "grad_norm": lambda: [dc.dynconv_grad_norm(tensors, 1.0, stats, number, nws, nws.numel(),
+                                                   st)],
+        "adamw": lambda: [dc.dynconv_adamw(tensors, hyper, grad_scale=stats[1:], step=number,
+                                           stream=st)],
+    }
+
+    def full():
+        for part in parts.values():
+            dc.check(part()[0])
+
+    def timed(fn):
+        with torch.cuda.stream(st):
+            for _ in range(max(args.warmup, 3)):
+                fn()
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        n0 = dc.dynconv_launch_count()
+        with torch.cuda.graph(g, stream=st):
+            fn()
+        launches = dc.dynconv_launch_count() - n0
+        g.replay()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        with torch.cuda.stream(st):
+            e0.record(st)
+            for _ in range(args.steps):
+                g.replay()
+            e1.record(st)
+        st.synchronize()
+        del g
+        return e0.elapsed_time(e1) / args.steps, launches
+
+    ms, launches = timed(full)
+    dc.check(dc.dynconv_device_status(st), "device status")
+    shares = {k: round(timed(lambda: dc.check(v()[0]))[0] * 1e3, 2) for k, v in parts.items()}
+    line = {"metric": "images/s (layer training step: route, balance loss, forward, backward, "
+                      "gradient norm, AdamW)",
+            "value": B / (ms / 1e3), "unit": "images/s", "n_gpus": 1, "steps": args.steps,
+            "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": "bf16" if bf16 else "f32",
+            "data": "synthetic (seeded normal draws, layer shapes of the configuration)",
+            "config": {"workload": f"{cfg.name} training step, {args.state_bits}-bit states",
+                       "l2": "one set of buffers, replayed (in L2 where it fits)"},
+            "us_per_call": shares, "gpu_launches_per_step": launches}
+    print(json.dumps(line), flush=True)
+    return 0
+
+
 def run_cells(args, cfg):
     """The layer with its kernel assembled from warehouse cells, one GPU: step =
     dynconv_route_cells + dynconv_forward_cells of one batch, CUDA graphs of 8
@@ -1147,6 +1264,8 @@ def main():
         return run_block(args)
     if args.backward:
         return run_backward(args, synth.CONFIGS[args.config or synth.HEADLINE])
+    if args.train:
+        return run_train(args, synth.CONFIGS[args.config or synth.HEADLINE])
     if args.cells:
         return run_cells(args, synth.CONFIGS[args.config or synth.HEADLINE])
     name = args.config or synth.HEADLINE

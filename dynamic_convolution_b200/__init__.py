@@ -414,17 +414,32 @@ def train_tensor(grad, param=None, m=None, v=None, master=None, m_scale=None, v_
         numel, dtype, F32 if grad.dtype is f32 else BF16, bits,
         float(lr_scale), float(weight_decay))
     entry.keeps = (param, master, grad, m, v, m_scale, v_scale)
+    entry.device = device.index if device.type == "cuda" else -1
     return entry
 
 
 def train_tensors(entries):
     """The list that dynconv_grad_norm and dynconv_adamw take. It holds the tensors'
     addresses and keeps the tensors of train_tensor entries alive; a tensor that is
-    replaced by another (not written in place) needs a new list."""
+    replaced by another (not written in place) needs a new list. All tensors are on
+    one device, which has to be the current one in the calls (else INVALID_ARG)."""
     entries = list(entries)
+    devices = {e.device for e in entries if hasattr(e, "device")}
+    if len(devices) > 1:
+        raise ValueError(f"tensors of one list are on several devices: {sorted(devices)}")
     array = (dynconv_train_tensor * len(entries))(*entries)
     array.keeps = [getattr(e, "keeps", None) for e in entries]
+    array.device = devices.pop() if devices else None
     return array
+
+
+def _elsewhere(tensors) -> bool:
+    """Whether a list's tensors are not on the current device (None: addresses only)."""
+    device = getattr(tensors, "device", None)
+    if device is None:
+        return False
+    import torch
+    return device < 0 or device != torch.cuda.current_device()
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0) -> dynconv_adamw_hyper:
@@ -442,6 +457,8 @@ def dynconv_grad_norm(tensors, max_norm, stats, step, workspace, workspace_bytes
                       stream=None) -> int:
     """stats fp32 [2] = {norm of all gradients, factor that clips it to max_norm};
     step int64 [1] (or None) is increased by one unless the norm is not finite."""
+    if _elsewhere(tensors):
+        return ERR_INVALID_ARG
     return load().dynconv_grad_norm(tensors, len(tensors), float(max_norm), _ptr(stats),
                                     _ptr(step), _ptr(workspace), int(workspace_bytes),
                                     _stream(stream))
@@ -450,5 +467,7 @@ def dynconv_grad_norm(tensors, max_norm, stats, step, workspace, workspace_bytes
 def dynconv_adamw(tensors, hyper, grad_scale=None, lr=None, step=None, stream=None) -> int:
     """One AdamW step over the list, in place; grad_scale, lr (fp32 [1]) and step
     (int64 [1]) on the device replace 1 and the values in hyper."""
+    if _elsewhere(tensors):
+        return ERR_INVALID_ARG
     return load().dynconv_adamw(tensors, len(tensors), ctypes.byref(hyper), _ptr(grad_scale),
                                 _ptr(lr), _ptr(step), _stream(stream))

@@ -295,6 +295,47 @@ def test_8_bit_states_follow_the_32_bit_ones():
     assert abs(b.m64.mean() / m32.mean() - 1) < 0.08
 
 
+@pytest.mark.parametrize("param,grad", [("bf16+master", "fp32"), ("bf16", "bf16")])
+def test_8_bit_states_are_the_fp32_formulas_bit_for_bit(param, grad):
+    """Five steps against separate fp32 operations of torch (IEEE products, sums,
+    square roots): every code and every scale, which also pins the kernel's own root
+    on a million values per step."""
+    n = 1 << 20
+    t = Tensor(n, param, grad, 8, seed=3)
+    m, v = t.m.t.float(), t.v.t.float()
+    ms, vs = t.ms.t.clone(), t.vs.t.clone()
+    b1, b2 = HYPER["beta1"], HYPER["beta2"]
+    gen = torch.Generator("cuda").manual_seed(1)
+
+    def store(x, u, positive):
+        x = x.view(-1, 256)
+        top = x.abs().amax(1)
+        inv = top.reciprocal() * 448.0
+        y = x.abs() * inv[:, None]
+        base = torch.where(y < 2.0 ** -6, 2.0 ** -6, 0.0)
+        q = (((y + base).view(torch.int32) + (u << 4)) & -(1 << 20)).view(torch.float32) - base
+        if positive:
+            q = torch.where(x > 0, q.clamp_min(2.0 ** -9), q)
+        return torch.copysign(q, x).view(-1), top * (1.0 / 448.0)
+
+    for step in range(1, 6):
+        g = (torch.randn(n, device="cuda", generator=gen) *
+             torch.exp(torch.randn(n, device="cuda", generator=gen)) * 1e-3)
+        t.grad.t.copy_(g)
+        g = t.grad.t.float()
+        dc.check(dc.dynconv_adamw(dc.train_tensors([t.entry()]),
+                                  dc.make_adamw(step=step, seed=9, **HYPER)))
+        u = torch.from_numpy((ref.dither(9, step, 0, n) * 65536).astype(np.int32)).cuda().view(-1, 256)
+        m32 = (m.view(-1, 256) * ms[:, None]).view(-1)
+        r32 = (v.view(-1, 256) * vs[:, None]).view(-1)
+        m32 = m32 * b1 + g * (1.0 - b1)
+        v32 = (r32 * r32) * b2 + (g * g) * (1.0 - b2)
+        m, ms = store(m32, u, False)
+        v, vs = store(v32.sqrt(), u, True)
+        assert torch.equal(t.m.t.float(), m) and torch.equal(t.v.t.float(), v)
+        assert torch.equal(t.ms.t, ms) and torch.equal(t.vs.t, vs)
+
+
 def test_the_same_inputs_give_the_same_bits():
     runs = []
     for _ in range(2):

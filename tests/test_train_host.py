@@ -198,6 +198,13 @@ def test_optimizer_without_a_device_fails_loudly():
     assert dc.dynconv_last_error() != ""
 
 
+def test_lists_of_tensors_on_the_host_are_refused():
+    f = lambda: torch.zeros(8)  # noqa: E731
+    tensors = dc.train_tensors([dc.train_tensor(grad=f(), param=f(), m=f(), v=f())])
+    assert dc.dynconv_adamw(tensors, dc.make_adamw(1e-3)) == dc.ERR_INVALID_ARG
+    assert dc.dynconv_grad_norm(tensors, 1.0, P, None, P, 1 << 20) == dc.ERR_INVALID_ARG
+
+
 def test_train_tensor_checks_what_it_is_given():
     f = lambda n=8, t=torch.float32: torch.zeros(n, dtype=t)  # noqa: E731
     e = dc.train_tensor(grad=f(), param=f(), m=f(), v=f(), weight_decay=0.5)
