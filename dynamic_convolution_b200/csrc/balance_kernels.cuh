@@ -348,15 +348,19 @@ __device__ __forceinline__ float lane_sum(const float (&a)[V]) {
   return x + y;
 }
 
-// p = a / total, and 0 where the total is 0: a reciprocal (relative error 2^-23) and
-// products, except where the reciprocal would leave fp32's normal numbers.
+// p = a / total, and 0 where the total is 0: a product with the reciprocal, corrected
+// by its residual (a row of one expert has p = 1 and no gradient left), except where
+// the reciprocal would leave fp32's normal numbers.
 template <int V>
 __device__ __forceinline__ void normalise(float (&a)[V], float total) {
   if (fabsf(total) >= 1e-30f && fabsf(total) <= 1e30f) {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
 #pragma unroll
-    for (int s = 0; s < V; ++s) a[s] *= inv;
+    for (int s = 0; s < V; ++s) {
+      const float q = a[s] * inv;
+      a[s] = fmaf(fmaf(-q, total, a[s]), inv, q);
+    }
   } else {
 #pragma unroll
     for (int s = 0; s < V; ++s) a[s] = total != 0.f ? __fdiv_rn(a[s], total) : 0.f;

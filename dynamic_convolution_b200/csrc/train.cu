@@ -63,7 +63,7 @@ int check_balance(const dynconv_balance_desc* d) {
   if (d->mode != DYNCONV_SIGMOID && d->mode != DYNCONV_SOFTMAX) return DYNCONV_ERR_INVALID_ARG;
   const long long width = 1LL * d->groups * d->n;
   if (d->row_stride < width) return DYNCONV_ERR_INVALID_ARG;
-  if (d->n > dct::kBalMaxN || width > 65536 || d->row_stride >= (1LL << 40) ||
+  if (d->n > dct::kBalMaxN || width > 65536 || d->groups > 65535 || d->row_stride >= (1LL << 40) ||
       (d->top_k > dct::kBalMaxTopK && d->top_k != d->n))
     return DYNCONV_ERR_UNSUPPORTED;
   return DYNCONV_OK;

@@ -49,9 +49,11 @@ extern "C" {
  *
  * and 0 on the rows that the mask drops, or with M = 0.
  *
- * rows >= 0; 1 <= n <= 1024; groups >= 1 with groups * n <= 65536;
+ * rows >= 0; 1 <= n <= 1024; 1 <= groups <= 65535 with groups * n <= 65536;
  * 1 <= top_k <= min(n, 32), or top_k = n; mode a dynconv_mode; row_stride >=
- * groups * n: floats from one row of alpha to the next (a row is contiguous). */
+ * groups * n: floats from one row of alpha to the next (a row is contiguous).
+ * Few rows (4096 attentions in the busiest of eight CTAs, n <= 256) take one
+ * launch, others two. */
 typedef struct {
   int rows, groups, n, top_k;
   int mode;
@@ -72,7 +74,8 @@ size_t dynconv_balance_workspace_size(const dynconv_balance_desc* desc);
  *   loss       fp32  [1]           (out)
  *   workspace  at least dynconv_balance_workspace_size bytes, 16-byte aligned;
  *              contents need not be preserved.
- * The sums over rows are taken in fp64.
+ * The sums over rows keep fp64's precision (fp32 pairs with their rounding
+ * errors, joined in fp64) and have a fixed order.
  * Errors: INVALID_ARG, UNSUPPORTED (a size above those limits), MISALIGNED (a
  * pointer not aligned to its element; the workspace), WORKSPACE, CUDA. */
 int dynconv_balance_forward(const dynconv_balance_desc* desc, const float* alpha,

@@ -237,6 +237,15 @@ def test_sigmoid_rows_that_sum_to_zero():
     assert torch.equal(c.dalpha[12:18].cpu(), torch.from_numpy(c.before[2]))
 
 
+def test_one_expert_leaves_no_gradient():
+    c = Case(5000, 1, 1, sigmoid=True, seed=4)
+    c.forward()
+    c.fill()
+    c.backward(0)
+    torch.cuda.synchronize()
+    assert not c.dalpha[:5000].any() and c.mean[:1].tolist() == [1.0]
+
+
 def test_default_dloss_and_repeatability():
     c = Case(1003, 48, 4, sigmoid=True, mask=0.6)
     c.forward()

@@ -59,7 +59,7 @@ def test_header_is_c_and_layouts_agree(tmp_path):
     (dict(groups=0), dc.ERR_INVALID_ARG), (dict(top_k=0), dc.ERR_INVALID_ARG),
     (dict(top_k=5), dc.ERR_INVALID_ARG), (dict(mode=2), dc.ERR_INVALID_ARG),
     (dict(row_stride=3), dc.ERR_INVALID_ARG), (dict(n=1025), dc.ERR_UNSUPPORTED),
-    (dict(n=64, top_k=33), dc.ERR_UNSUPPORTED), (dict(n=1024, groups=65), dc.ERR_UNSUPPORTED),
+    (dict(n=1, groups=65536), dc.ERR_UNSUPPORTED), (dict(n=64, top_k=33), dc.ERR_UNSUPPORTED), (dict(n=1024, groups=65), dc.ERR_UNSUPPORTED),
     (dict(row_stride=1 << 40), dc.ERR_UNSUPPORTED)])
 def test_balance_descriptors_refused(kw, code):
     d = dc.make_balance_desc(**{**dict(rows=8, n=4), **kw})
