@@ -556,7 +556,11 @@ __device__ __forceinline__ void group_sums(const BalParams& p, int j, long long 
   __syncthreads();
 }
 
-// One part of the sums of one group (blockIdx.y).
+// One part of the sums of one group (blockIdx.y). Reads the attentions once; bound by
+// instruction issue, most of it the choice of the top k: 1 M rows of 16 sigmoid
+// attentions, top 2, a fifth masked: 33 us (64 MB; 19 us without the choice); 30 K rows
+// of 1000, top 8: 50 us (96 MB; 29 without it; 67 before the lanes' maxima filtered the
+// candidates and while 512 threads spilled registers).
 template <int L, int V, int T>
 __global__ void __launch_bounds__(T)
 balance_forward_kernel(BalParams p) {
@@ -605,8 +609,8 @@ __device__ __forceinline__ double loss_factor(float coef, int n, int top_k, int 
 }
 
 // Few rows: the whole forward in one launch of one cluster, which takes the
-// groups in turn and meets only for the loss (a launch less: 4 of 13 us of a
-// forward and backward over 64 rows).
+// groups in turn and meets only for the loss (64 rows of 4 experts, forward and
+// backward: 10.1 us for 12.8 with a finishing launch; bound by the calls).
 template <int L, int V, int THREADS>
 __global__ void __launch_bounds__(THREADS) balance_small_kernel(BalParams p) {
   __shared__ BalShared sh;
@@ -749,7 +753,8 @@ __device__ __forceinline__ double slope_of(const BalBack& p) {
 }
 
 // SOFTMAX: the same row of coefficients on every kept row. A thread owns four
-// columns and walks down the rows.
+// columns and walks down the rows. Bound by memory: 30 K rows of 1000, added to
+// dalpha, 30 us (6.4 TB/s).
 __global__ void __launch_bounds__(kBalThreads) balance_backward_softmax_kernel(BalBack p, int tx) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ty = kBalThreads / tx;
@@ -783,6 +788,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_softmax_kernel(B
 }
 
 // SIGMOID: (c - sum_l c_l p_l) / S of every kept row; rows held as in the forward.
+// 1 M rows of 16, added to dalpha: 36 us (154 MB of kept rows, 4.3 TB/s).
 template <int L, int V>
 __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(BalBack p) {
   constexpr int R = 32 / L;
