@@ -22,6 +22,8 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t align16(size_t v) { return (v + 15) & ~size_t(15); }
+// Units that hold `total` items (64 bits throughout: rows and elements reach 2^31).
+long long units_of(long long total, long long unit) { return (total + unit - 1) / unit; }
 
 // Launch with a programmatic edge: the kernel may be scheduled while the
 // previous one on the stream finishes, and waits for it (griddepcontrol.wait)
@@ -93,7 +95,7 @@ struct BalSplit {
 };
 BalSplit balance_split(const dynconv_balance_desc* d) {
   const int lanes = row_lanes(d->n);
-  const auto ctas = [&](int threads) { return (d->rows + threads / lanes - 1LL) / (threads / lanes); };
+  const auto ctas = [&](int threads) { return units_of(d->rows, threads / lanes); };
   BalSplit s;
   s.threads = dct::forward_threads(d->n <= 256 ? 8 : d->n <= 512 ? 16 : 32);
   int most = 148;
@@ -247,8 +249,6 @@ int check_state(const dynconv_train_tensor& t) {
   return DYNCONV_OK;
 }
 
-long long units_of(long long numel, long long unit) { return (numel + unit - 1) / unit; }
-
 // Four elements of the type are one load of 4 * size bytes.
 bool vec_ok(const void* p, size_t elem) { return aligned(p, 4 * elem); }
 
@@ -381,8 +381,7 @@ int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alph
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sigmoid) {
     p.vec = p.vec && aligned(alpha, 16) && desc->row_stride % 4 == 0 && desc->n % 4 == 0;
-    const long long per = kBalWarps * (32 / row_lanes(desc->n));
-    const long long want = (desc->rows + per - 1) / per;
+    const long long want = units_of(desc->rows, kBalWarps * (32 / row_lanes(desc->n)));
     const int grid = static_cast<int>(
         std::min<long long>(want, std::max(1LL, 8LL * di.sms / desc->groups)));
     return with_layout(desc->n, LaunchSigmoid{dim3(grid, desc->groups), s, p});
@@ -392,7 +391,7 @@ int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alph
   int tx = 1;
   while (tx < vecs && tx < dct::kBalThreads) tx *= 2;
   const int gy = (vecs + tx - 1) / tx, ty = dct::kBalThreads / tx;
-  const long long want = (desc->rows + ty - 1) / ty;
+  const long long want = units_of(desc->rows, ty);
   const int gx = static_cast<int>(std::min<long long>(want, std::max(1LL, 8LL * di.sms / gy)));
   return launch("balance_backward_softmax_kernel", dct::balance_backward_softmax_kernel,
                 dim3(gx, gy), dct::kBalThreads, 0, s, p, tx);
@@ -400,7 +399,7 @@ int dynconv_balance_backward(const dynconv_balance_desc* desc, const float* alph
 
 size_t dynconv_grad_norm_workspace_size(int count) {
   if (count < 0) return 0;
-  const size_t launches = std::max(1, (count + dct::kNormCap - 1) / dct::kNormCap);
+  const size_t launches = std::max(1LL, units_of(count, dct::kNormCap));
   return launches * dct::kNormParts * sizeof(double);
 }
 
