@@ -336,10 +336,22 @@ def dynconv_forward_cells(desc, cells, x, warehouse, alpha, bias, y, workspace, 
 # ------------------------------------------------------------------ training
 
 
+def _fit(name, value, bits=32):
+    """`value` as an int, which ctypes would cut off to the field's bits."""
+    value = int(value)
+    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+        raise ValueError(f"{name}: {value} does not fit {bits} bits")
+    return value
+
+
 def make_balance_desc(rows, n, groups=1, top_k=1, mode=SOFTMAX,
                       row_stride=None) -> dynconv_balance_desc:
-    return dynconv_balance_desc(int(rows), int(groups), int(n), int(top_k), int(mode),
-                                int(groups) * int(n) if row_stride is None else int(row_stride))
+    """Descriptor of a router's attentions (row_stride: groups * n unless given); a
+    number that its field does not hold raises ValueError."""
+    rows, groups, n = _fit("rows", rows), _fit("groups", groups), _fit("n", n)
+    stride = groups * n if row_stride is None else row_stride
+    return dynconv_balance_desc(rows, groups, n, _fit("top_k", top_k), _fit("mode", mode),
+                                _fit("row_stride", stride, 64))
 
 
 def dynconv_balance_workspace_size(desc) -> int:
@@ -443,8 +455,10 @@ def _elsewhere(tensors) -> bool:
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0) -> dynconv_adamw_hyper:
-    return dynconv_adamw_hyper(float(lr), float(beta1), float(beta2), float(eps), int(step),
-                               int(seed) & 0xFFFFFFFF)
+    """Hyper-parameters of a step (seed: its low 32 bits); a step number that 64 bits
+    do not hold raises ValueError."""
+    return dynconv_adamw_hyper(float(lr), float(beta1), float(beta2), float(eps),
+                               _fit("step", step, 64), int(seed) & 0xFFFFFFFF)
 
 
 def dynconv_grad_norm_workspace_size(tensors) -> int:

@@ -26,3 +26,22 @@ def test_balance_split_of_rows_up_to_the_types_last(n):
 def test_norm_workspace_of_any_count(count):
     """1184 fp64 parts for every 768 tensors begun, and for none."""
     assert dc.dynconv_grad_norm_workspace_size(count) == 8 * 1184 * max(1, -(-count // 768))
+
+
+@pytest.mark.parametrize("kw", [dict(rows=2**32 + 8), dict(rows=2**31), dict(rows=-2**31 - 1),
+                                dict(n=2**32 + 4), dict(groups=2**32 + 1), dict(top_k=2**32 + 1),
+                                dict(mode=2**32), dict(row_stride=2**64 + 4)])
+def test_numbers_that_a_descriptor_cannot_hold_are_refused(kw):
+    """(2^32 + 8 rows would be taken for 8.)"""
+    good = dict(rows=8, n=4)
+    assert dc.make_balance_desc(**good).rows == 8
+    assert dc.make_balance_desc(2**31 - 1, 4).rows == 2**31 - 1
+    with pytest.raises(ValueError):
+        dc.make_balance_desc(**{**good, **kw})
+
+
+def test_step_numbers_that_64_bits_cannot_hold_are_refused():
+    assert dc.make_adamw(1e-3, step=2**63 - 1, seed=2**32 + 3).step == 2**63 - 1
+    assert dc.make_adamw(1e-3, seed=2**32 + 3).seed == 3
+    with pytest.raises(ValueError):
+        dc.make_adamw(1e-3, step=2**64 + 1)
