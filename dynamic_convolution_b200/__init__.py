@@ -434,7 +434,8 @@ def train_tensors(entries):
     """The list that dynconv_grad_norm and dynconv_adamw take. It holds the tensors'
     addresses and keeps the tensors of train_tensor entries alive; a tensor that is
     replaced by another (not written in place) needs a new list. All tensors are on
-    one device, which has to be the current one in the calls (else INVALID_ARG)."""
+    one device, which has to be the current one in the calls and the device of the
+    calls' other tensors (else INVALID_ARG)."""
     entries = list(entries)
     devices = {e.device for e in entries if hasattr(e, "device")}
     if len(devices) > 1:
@@ -445,9 +446,17 @@ def train_tensors(entries):
     return array
 
 
-def _elsewhere(tensors) -> bool:
-    """Whether a list's tensors are not on the current device (None: addresses only)."""
+def _elsewhere(tensors, *others) -> bool:
+    """Whether a list's tensors, or torch tensors among the others, are not all on the
+    current device (addresses are taken as they are)."""
     device = getattr(tensors, "device", None)
+    for t in others:
+        if t is not None and not isinstance(t, int):
+            at = t.get_device()   # -1 on the host
+            if device is None:
+                device = at
+            elif at != device:
+                return True
     if device is None:
         return False
     import torch
@@ -471,7 +480,7 @@ def dynconv_grad_norm(tensors, max_norm, stats, step, workspace, workspace_bytes
                       stream=None) -> int:
     """stats fp32 [2] = {norm of all gradients, factor that clips it to max_norm};
     step int64 [1] (or None) is increased by one unless the norm is not finite."""
-    if _elsewhere(tensors):
+    if _elsewhere(tensors, stats, step, workspace):
         return ERR_INVALID_ARG
     return load().dynconv_grad_norm(tensors, len(tensors), float(max_norm), _ptr(stats),
                                     _ptr(step), _ptr(workspace), int(workspace_bytes),
@@ -481,7 +490,7 @@ def dynconv_grad_norm(tensors, max_norm, stats, step, workspace, workspace_bytes
 def dynconv_adamw(tensors, hyper, grad_scale=None, lr=None, step=None, stream=None) -> int:
     """One AdamW step over the list, in place; grad_scale, lr (fp32 [1]) and step
     (int64 [1]) on the device replace 1 and the values in hyper."""
-    if _elsewhere(tensors):
+    if _elsewhere(tensors, grad_scale, lr, step):
         return ERR_INVALID_ARG
     return load().dynconv_adamw(tensors, len(tensors), ctypes.byref(hyper), _ptr(grad_scale),
                                 _ptr(lr), _ptr(step), _stream(stream))

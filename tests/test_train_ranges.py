@@ -2,6 +2,7 @@
 without a GPU: sizes near the integer types' last values, arguments that do not
 fit."""
 import pytest
+import torch
 
 import dynamic_convolution_b200 as dc
 from dynamic_convolution_b200 import build as dcbuild
@@ -45,3 +46,17 @@ def test_step_numbers_that_64_bits_cannot_hold_are_refused():
     assert dc.make_adamw(1e-3, seed=2**32 + 3).seed == 3
     with pytest.raises(ValueError):
         dc.make_adamw(1e-3, step=2**64 + 1)
+
+
+def test_host_tensors_in_place_of_device_scalars_are_refused():
+    """A rate, a step number, a factor or a workspace left on the host would be read by
+    the kernels through its host address."""
+    P = 256   # an aligned address that is never read
+    entry = dc.dynconv_train_tensor(P, None, P, P, P, None, None, 0, dc.F32, dc.F32, 32, 1.0, 0.0)
+    tensors, hyper = dc.train_tensors([entry]), dc.make_adamw(1e-3)
+    one, number = torch.ones(1), torch.ones(1, dtype=torch.int64)
+    for kw in (dict(lr=one), dict(grad_scale=one), dict(step=number)):
+        assert dc.dynconv_adamw(tensors, hyper, **kw) == dc.ERR_INVALID_ARG
+    byte = torch.empty(1 << 20, dtype=torch.uint8)
+    for stats, step, ws in ((torch.zeros(2), None, P), (P, number, P), (P, None, byte)):
+        assert dc.dynconv_grad_norm(tensors, 1.0, stats, step, ws, 1 << 20) == dc.ERR_INVALID_ARG
