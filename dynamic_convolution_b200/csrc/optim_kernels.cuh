@@ -292,11 +292,16 @@ __device__ __forceinline__ Pair add_apart(Pair a, Pair b) {
   unpair(b, b0, b1);
   return pair_of(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
 }
-// Two square roots by Newton's method: with y near 1 / sqrt(x), r = x y is near the
-// root, x - r^2 is exact in one multiply-add, and r + (x - r^2) y / 2 is within
-// 2^-20 of a unit in the last place of the root before its rounding, so that it is
-// the correctly rounded root but for about one value in a million. For x from 2^-100
-// (below, the residual would be subnormal) to the largest finite number.
+// Two square roots by Newton's method. With y = (1 + e) / sqrt(x), |e| <= 2^-22.9 (the
+// instruction's documented bound), r = x y is the root times 1 + d, |d| <= 2^-22.3 with
+// the product's rounding; x - r^2, one multiply-add, is -x (2 d + d^2) but for its own
+// rounding of 2^-24; so r + (x - r^2) y / 2 is off the root by at most
+// |d| (|d| / 2 + |e| + 2^-24) < 2^-44 of it before it is rounded, 2^-20 of a unit in the
+// last place. That rounds to the correctly rounded root unless the root lies as close as
+// that to the border between two numbers, which about forty of the 2^24 mantissas (of
+// both exponent parities) have it do; the tests find the right root at those too, over
+// all exponents. For x from 2^-100 (from there on down the residual's last bits go below
+// fp32's least number) to the largest finite number.
 __device__ __forceinline__ Pair sqrt2(float lo, float hi) {
   const Pair x = pair_of(lo, hi), y = pair_of(rsqrt_approx(lo), rsqrt_approx(hi));
   const Pair r = x * y;
