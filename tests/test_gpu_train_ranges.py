@@ -49,6 +49,92 @@ def test_as_many_rows_as_the_type_holds(sigmoid):
     assert low == high and abs(low - want) <= 2 * E * want and float(c.dalpha[rows]) == 5.0
 
 
+@pytest.fixture
+def sorted_reference(monkeypatch):
+    """train_ref.balance with its top k from one stable sort (NaN last), for many rows."""
+    def balance(alpha, mask, k, sigmoid, coef):
+        rows, groups, n = alpha.shape
+        a = torch.from_numpy(alpha if mask is None else alpha[mask.astype(bool)]).cuda()
+        M = a.shape[0]
+        key = torch.where(a.isnan(), -float("inf"), a)
+        chosen = torch.sort(key, dim=-1, descending=True, stable=True).indices[..., :k]
+        counts = torch.zeros(groups, n, dtype=torch.int64, device="cuda")
+        counts.scatter_add_(1, chosen.transpose(0, 1).reshape(groups, M * k),
+                            torch.ones(groups, M * k, dtype=torch.int64, device="cuda"))
+        p = a / a.sum(-1, keepdim=True) if sigmoid else a
+        mean = p.sum(0) / max(M, 1)
+        loss = coef * n / (k * groups) * float((counts / max(M, 1) * mean).sum())
+        return dict(counts=counts.cpu().numpy(), mean=mean.cpu().numpy(), kept=M, loss=loss)
+
+    a = np.round(np.random.default_rng(0).random((40, 2, 9)) * 6) / 6
+    mask = np.arange(40) % 3
+    x, y = balance(a, mask, 3, True, 0.5), ref.balance(a, mask, 3, True, 0.5)
+    assert np.array_equal(x["counts"], y["counts"]) and x["kept"] == y["kept"]
+    assert np.allclose(x["mean"], y["mean"], rtol=1e-13) and np.isclose(x["loss"], y["loss"])
+    monkeypatch.setattr(ref, "balance", balance)
+
+
+# rows: beyond one turn of 148 CTAs of 1024, 512 or 384 threads, whose warps hold 32 / L rows
+# (L = 1, 1, 2, 4, 8, 16, 32, 32, then 32 with 16 or 32 values a lane)
+LONG = [(3, 160_001, 0), (8, 160_001, 0), (15, 80_011, 1), (16, 80_011, 4), (32, 40_009, 0),
+        (33, 20_011, 0), (64, 20_011, 8), (100, 10_007, 4), (200, 10_007, 0), (256, 15_001, 0)]
+WIDE = [(300, 7103, 4), (511, 7103, 0), (512, 7103, 0), (999, 5329, 0), (1000, 5329, 24),
+        (1024, 5329, 0)]
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("n,rows,pad", LONG + WIDE)
+def test_several_turns_with_masked_rows(sorted_reference, n, rows, pad, sigmoid):
+    Case(rows, n, min(n - 1, 5), sigmoid=sigmoid, mask=0.7, pad=pad, seed=n).run()
+
+
+@pytest.mark.parametrize("kept", [0.04, 1.0])
+@pytest.mark.parametrize("n,rows,pad", [(16, 80_011, 0), (512, 7103, 0), (1000, 5329, 0)])
+def test_several_turns_with_few_rows_kept_and_with_all(sorted_reference, n, rows, pad, kept):
+    Case(rows, n, 4, sigmoid=True, mask=kept, pad=pad, seed=n).run()
+
+
+@pytest.mark.parametrize("n,rows", [(16, 80_011), (200, 10_007), (300, 7103), (1000, 5329)])
+def test_several_turns_with_ties(sorted_reference, n, rows):
+    Case(rows, n, 7, mask=0.8, ties=True, seed=n).run()
+
+
+@pytest.mark.parametrize("n,rows,groups,pad", [(4, 40_003, 5, 0), (100, 2003, 40, 0),
+                                               (24, 3001, 100, 3), (12, 1500, 200, 0),
+                                               (1000, 601, 3, 0)])
+def test_several_turns_of_several_groups(sorted_reference, n, rows, groups, pad):
+    Case(rows, n, 3, groups=groups, sigmoid=True, mask=0.7, pad=pad, seed=n).run()
+
+
+@pytest.mark.parametrize("n,rows", [(16, 80_011), (100, 10_007), (512, 7103), (1000, 5329)])
+def test_nan_in_rows_of_every_turn(sorted_reference, n, rows):
+    """Some NaN in kept rows, and rows with fewer than k numbers left, between masked ones."""
+    k = 6
+    c = Case(rows, n, k, mask=0.8, seed=n)
+    rng = np.random.default_rng(n)
+    for r in range(0, rows, 97):
+        gone = 2 if r % 2 else n - k + 2
+        c.a[r, 0, rng.permutation(n)[:gone]] = np.nan
+    kept = torch.from_numpy(c.mask != 0).cuda()
+    held = c.alpha[:rows * n].view(rows, n)
+    held[kept] = torch.from_numpy(c.a[:, 0].astype(np.float32)).cuda()[kept]
+    c.forward()
+    torch.cuda.synchronize()
+    want = ref.balance(c.a, c.mask, k, False, COEF)
+    assert np.array_equal(c.counts[:n].cpu().numpy(), want["counts"][0])
+    assert bool(torch.isnan(c.loss[0])) and int(c.kept[0]) == want["kept"]
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("n,rows,groups", [(1, 4096, 1), (2, 2047, 8), (3, 1365, 3), (4, 1024, 8),
+                                           (4, 1024, 16), (4, 32, 256), (4, 2, 1024), (1, 1, 4096),
+                                           (3, 7, 300)])
+def test_one_launch_over_several_turns_and_many_groups(sorted_reference, n, rows, groups, sigmoid):
+    """(The fifth is a size beyond the one launch.)"""
+    Case(rows, n, 1, groups=groups, sigmoid=sigmoid, mask=0.8 if rows > 2 else None,
+         seed=rows).run()
+
+
 # --------------------------------------------------------------------- roots
 
 
