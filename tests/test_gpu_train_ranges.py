@@ -10,6 +10,7 @@ import dynamic_convolution_b200 as dc
 
 from . import train_ref as ref
 from .test_gpu_balance import COEF, Case
+from .test_gpu_optim import HYPER, KINDS, Tensor
 
 pytestmark = pytest.mark.gpu
 E = ref.E
@@ -232,3 +233,104 @@ def test_8_bit_roots_of_the_last_numbers():
     v = g * g
     assert np.isfinite(v).all()
     check_roots(v.astype(np.float64), np.zeros(len(g), np.float32), g, 0.0)
+
+
+# ------------------------------------------------------------------- the norm
+
+
+PIECE, CTAS = 4096, 1184   # elements of a piece, CTAs of a launch at most
+
+
+def way_through(sizes):
+    """How the CTAs of one launch get from unit to unit: a count of the steps that stay in
+    a tensor and of those to the next one, to the one after it and further on."""
+    pieces = sum(-(-s // PIECE) for s in sizes)
+    per = max(1, min(2, pieces // (2 * CTAS)))
+    of = np.repeat(np.arange(len(sizes)), [-(-s // (per * PIECE)) for s in sizes])
+    hop = np.minimum(of[CTAS:] - of[:-CTAS], 3)
+    return per, np.bincount(hop, minlength=4)
+
+
+def sizes_in(pieces, ragged):
+    return [max(1, PIECE * k - (i * 577 % 4095 if ragged else 0)) for i, k in enumerate(pieces)]
+
+
+NORM_LISTS = {
+    # one piece a unit (fewer than 2368 x 2 pieces), two pieces, and two with single pieces last
+    "short": ([1300, 700, 500, 300] + [40] * 12 + [3] * 50 + [1] * 150 + [600], 1),
+    "long": ([5000, 2500, 1200, 900, 700] + [90] * 20 + [7] * 60 + [1] * 100 + [2400, 300], 2),
+    "long with a small end": ([4800, 3] + [601, 602] * 4 + [1] * 600 + [5], 2),
+}
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("name", NORM_LISTS)
+def test_norm_of_lists_whose_units_cross_tensors(name, ragged):
+    """Mixed types and starts on and off the 16-byte grid, values between 1/2 and 1. Each
+    tensor in turn is raised by 2^30, so that the norm is that tensor's alone: the others
+    have at most 2^26 elements, less than 2^-32 of its square."""
+    sizes = sizes_in(NORM_LISTS[name][0], ragged)
+    per, hops = way_through(sizes)
+    assert per == NORM_LISTS[name][1] and (hops[:2] > 0).all() and len(sizes) <= 768
+    gen = torch.Generator("cuda").manual_seed(len(sizes))
+    grads = []
+    for i, k in enumerate(sizes):
+        g = torch.rand(k + 8, device="cuda", generator=gen) / 2 + 0.5
+        g = g.bfloat16() if i % 3 == 1 else g
+        grads.append(g[1:k + 1] if i % 4 == 3 else g[:k])
+    tensors = dc.train_tensors(dc.train_tensor(grad=g) for g in grads)
+    size = dc.dynconv_grad_norm_workspace_size(tensors)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    squares = torch.stack([g.double().square().sum() for g in grads])
+    stats = torch.empty(len(grads) + 1, 2, device="cuda")
+    for i in range(len(grads) + 1):
+        if i < len(grads):
+            grads[i].mul_(2.0**30)
+        dc.check(dc.dynconv_grad_norm(tensors, 1.0, stats[i], None, ws, size))
+        if i < len(grads):
+            grads[i].mul_(2.0**-30)
+    raised = squares.sum() + squares * (2.0**60 - 1)
+    want = torch.cat([raised, squares.sum().view(1)]).sqrt()
+    assert bool(((stats[:, 0].double() - want).abs() <= 1.01 * E * want).all())
+
+
+def test_the_norms_lists_take_every_way():
+    """Between them the lists above make each kind of step, with units of one piece and of two."""
+    seen = {1: np.zeros(4, int), 2: np.zeros(4, int)}
+    for pieces, _ in NORM_LISTS.values():
+        for ragged in (False, True):
+            per, hops = way_through(sizes_in(pieces, ragged))
+            seen[per] += hops
+    assert all((hops > 0).all() for hops in seen.values())
+
+
+def test_lists_of_several_launches_captured_and_replayed():
+    """800 tensors: two launches of the norm, three of AdamW, 32 KB of parameters each; the
+    graph keeps its own lists."""
+    sets = [[Tensor(1 + (i * 37) % 600, *KINDS[i % len(KINDS)], seed=i) for i in range(800)]
+            for _ in range(2)]
+    side = torch.cuda.Stream()
+    stats = [torch.zeros(2, device="cuda") for _ in sets]
+    steps = [torch.zeros(1, dtype=torch.int64, device="cuda") for _ in sets]
+    lists = [dc.train_tensors(x.entry() for x in t) for t in sets]
+    size = dc.dynconv_grad_norm_workspace_size(lists[0])
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+
+    def step(i):
+        dc.check(dc.dynconv_grad_norm(lists[i], 0.5, stats[i], steps[i], ws, size, side))
+        dc.check(dc.dynconv_adamw(lists[i], dc.make_adamw(**HYPER, seed=4), stats[i][1:],
+                                  step=steps[i], stream=side))
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(0)
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            graph.replay()
+        step(1)
+    side.synchronize()
+    assert torch.equal(*stats) and steps[0].tolist() == [2] == steps[1].tolist()
+    for a, b in zip(*sets):
+        assert all(torch.equal(x, y) for x, y in zip(a.state(), b.state()))
+    del graph
