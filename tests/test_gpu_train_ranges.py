@@ -10,7 +10,7 @@ import dynamic_convolution_b200 as dc
 
 from . import train_ref as ref
 from .test_gpu_balance import COEF, Case
-from .test_gpu_optim import HYPER, KINDS, Tensor
+from .test_gpu_optim import HYPER, KINDS, Tensor, step_and_check
 
 pytestmark = pytest.mark.gpu
 E = ref.E
@@ -334,3 +334,13 @@ def test_lists_of_several_launches_captured_and_replayed():
     for a, b in zip(*sets):
         assert all(torch.equal(x, y) for x, y in zip(a.state(), b.state()))
     del graph
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_steps_whose_chunks_cross_tensors_of_other_types(order):
+    """444 CTAs (with 8-bit states) go from tensor to tensor of every kind, with one, two
+    or no chunks of 2048 in each: the staged inputs of one type follow those of another."""
+    sizes = (1_000_003, 300_001, 5000, 920_000, 70_001, 2_100_000)
+    tensors = [Tensor(sizes[i % 6], *kind, shift=i % 5 == 4, seed=i)
+               for i, kind in enumerate((KINDS[1::2] + KINDS[::2])[::order] + KINDS[1::2])]
+    step_and_check(tensors)
