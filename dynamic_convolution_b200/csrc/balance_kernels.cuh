@@ -753,8 +753,9 @@ __device__ __forceinline__ double slope_of(const BalBack& p) {
 }
 
 // SOFTMAX: the same row of coefficients on every kept row. A thread owns four
-// columns and walks down the rows. Bound by memory: 30 K rows of 1000, added to
-// dalpha, 30 us (6.4 TB/s).
+// columns and walks down the rows. Bound by memory: 30 K rows of 1000, a fifth masked,
+// added to dalpha, 30 us (6.4 TB/s). Rows off the 16-byte grid take four single words in
+// place of each 16 bytes: all 30 K rows 123 us at 999 experts, 47 at 1000.
 __global__ void __launch_bounds__(kBalThreads) balance_backward_softmax_kernel(BalBack p, int tx) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ty = kBalThreads / tx;
@@ -789,7 +790,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_softmax_kernel(B
 
 // SIGMOID: (c - sum_l c_l p_l) / S of every kept row; rows held as in the forward.
 // 1 M rows of 16, added to dalpha: 33 us (154 MB of kept rows, 4.7 TB/s; 36 with
-// dalpha read where it is added to).
+// dalpha read where it is added to). Bound by the latency of its loads: with 56
+// registers half of the warps are resident, each with one group of rows under way
+// (waiting for loads takes 10 of the 17 cycles between a warp's instructions). Rows off
+// the 16-byte grid: 53 us at 15 experts, 72 at 17, by accesses of single words.
+// The quotient by the row's sum is a product with the one-instruction reciprocal
+// (2^-23 relative, two half steps more than a division's; the forward corrects its own
+// because a single expert's probability has to be exactly 1).
 template <int L, int V>
 __global__ void __launch_bounds__(kBalThreads) balance_backward_sigmoid_kernel(BalBack p) {
   constexpr int R = 32 / L;

@@ -82,7 +82,9 @@ int row_lanes(int n) {
 
 // The whole forward in one launch of one cluster of up to eight CTAs of 256 or
 // 1024 threads, each taking every eighth group: while the busiest of them has at
-// most 4 K attentions of at most 256 experts.
+// most 4 K attentions of at most 256 experts. (64 rows of 4 in one group: forward and
+// backward 10.1 us, 12.8 with two launches. The groups of a CTA come one after another,
+// about 2 us each: 2 rows of 4 in 16 groups 8 us, in 64 groups 18, in 1024 groups 231.)
 bool balance_small(const dynconv_balance_desc* d) {
   const long long turns = (d->groups + dct::kBalCluster - 1) / dct::kBalCluster;
   return d->n <= 256 && turns * d->rows * d->n <= 4096;

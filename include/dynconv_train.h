@@ -12,6 +12,9 @@
  * dynconv_backward_weight, dynconv_balance_backward (adds to dalpha),
  * dynconv_route_backward, dynconv_backward_data; the sum over ranks;
  * dynconv_grad_norm, dynconv_adamw.
+ * Warehouse cells are forward only (dynconv_cells.h): the balance loss and counts of
+ * dynconv_route_cells' attentions are there to watch, and its gradient for a backward
+ * of the caller's own; no call of this library takes it further.
  *
  * Conventions are those of dynconv.h: device pointers owned by the caller, work
  * enqueued on `stream` of the current device, nothing allocated, arguments
@@ -53,7 +56,8 @@ extern "C" {
  * 1 <= top_k <= min(n, 32), or top_k = n; mode a dynconv_mode; row_stride >=
  * groups * n: floats from one row of alpha to the next (a row is contiguous).
  * Few rows (4096 attentions in the busiest of eight CTAs, n <= 256) take one
- * launch, others two. */
+ * launch, others two. coef is fp32 like the tensors it scales: 0.01 is taken as the
+ * nearest fp32 number, 2.2e-8 of it away, and the results follow that number. */
 typedef struct {
   int rows, groups, n, top_k;
   int mode;
