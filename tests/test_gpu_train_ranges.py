@@ -2,11 +2,15 @@
 small cases do not reach: several turns of every kernel's main loop, the last sizes
 of the types, lists whose units cross from tensor to tensor, roots next to a
 rounding's border."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import dynamic_convolution_b200 as dc
+from dynamic_convolution_b200.build import ROOT
 
 from . import train_ref as ref
 from .test_gpu_balance import COEF, Case
@@ -129,9 +133,9 @@ def test_nan_in_rows_of_every_turn(sorted_reference, n, rows):
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("n,rows,groups", [(1, 4096, 1), (2, 2047, 8), (3, 1365, 3), (4, 1024, 8),
                                            (4, 1024, 16), (4, 32, 256), (4, 2, 1024), (1, 1, 4096),
-                                           (3, 7, 300)])
+                                           (3, 7, 300), (1, 5, 65535), (16, 3, 4096)])
 def test_one_launch_over_several_turns_and_many_groups(sorted_reference, n, rows, groups, sigmoid):
-    """(The fifth is a size beyond the one launch.)"""
+    """(The fifth is a size beyond the one launch, the last two the most groups and columns.)"""
     Case(rows, n, 1, groups=groups, sigmoid=sigmoid, mask=0.8 if rows > 2 else None,
          seed=rows).run()
 
@@ -344,3 +348,41 @@ def test_steps_whose_chunks_cross_tensors_of_other_types(order):
     tensors = [Tensor(sizes[i % 6], *kind, shift=i % 5 == 4, seed=i)
                for i, kind in enumerate((KINDS[1::2] + KINDS[::2])[::order] + KINDS[1::2])]
     step_and_check(tensors)
+
+
+COLD = """
+import torch
+import dynamic_convolution_b200 as dc
+f = lambda *s: torch.rand(s, device="cuda")
+alpha, dalpha, mean, loss = f(5000, 300), f(5000, 300), f(300), f(1)
+counts, kept = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (300, 1))
+desc = dc.make_balance_desc(5000, 300, top_k=4, mode=dc.SIGMOID)
+ws = torch.empty(dc.dynconv_balance_workspace_size(desc), dtype=torch.uint8, device="cuda")
+byte = lambda: torch.zeros(3000, dtype=torch.uint8, device="cuda")
+tensors = dc.train_tensors([
+    dc.train_tensor(grad=f(3000), param=f(3000), m=f(3000), v=f(3000)),
+    dc.train_tensor(grad=f(3000), param=f(3000), m=byte(), v=byte(), m_scale=f(12), v_scale=f(12))])
+nws = torch.empty(dc.dynconv_grad_norm_workspace_size(tensors), dtype=torch.uint8, device="cuda")
+stats, step = f(2), torch.zeros(1, dtype=torch.int64, device="cuda")
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=side):
+    dc.check(dc.dynconv_balance_forward(desc, alpha, None, 0.01, counts, mean, kept, loss, ws,
+                                        ws.numel(), side))
+    dc.check(dc.dynconv_balance_backward(desc, alpha, None, 0.01, counts, kept, None, dalpha, 300,
+                                         0, side))
+    dc.check(dc.dynconv_grad_norm(tensors, 1.0, stats, step, nws, nws.numel(), side))
+    dc.check(dc.dynconv_adamw(tensors, dc.make_adamw(1e-3), stats[1:], step=step, stream=side))
+graph.replay()
+torch.cuda.synchronize()
+print(int(kept), int(counts.sum()), int(step))
+del graph
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing has to run before a capture (kernels loaded, attributes set, state queried)."""
+    run = subprocess.run([sys.executable, "-c", COLD], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    assert run.stdout.split() == ["5000", "20000", "1"]
